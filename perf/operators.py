@@ -332,8 +332,11 @@ def _attn_plain(st):
     c = st["case"]
     G, D, R = c["heads"], c["dim"], c["rope"]
     slot, ok = _selected(st)
-    k = st["codes"].view(-1, D).view(torch.uint8)[slot].view(torch.float8_e4m3fn).float()
-    k *= st["descale"].view(-1)[slot].unsqueeze(-1)          # [rows, topk, D]
+    codes, descale = st["codes"].view(-1, D), st["descale"].view(-1)
+    if slot.numel() > codes.shape[0]:                        # prefill: the cache once, then rows
+        k = (codes.float() * descale[:, None])[slot]
+    else:                                                    # decode: the selected rows only
+        k = codes.view(torch.uint8)[slot].view(codes.dtype).float() * descale[slot].unsqueeze(-1)
     x = torch.bmm(st["q"].reshape(-1, G, D).float(), k.transpose(1, 2))
     if R:
         kr = st["kr"].view(-1, R)[slot].float()
