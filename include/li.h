@@ -414,6 +414,133 @@ li_status li_sparse_attention_workspace_size(const li_attn_args *args, size_t *b
 li_status li_sparse_attention(const li_attn_args *args, void *workspace, size_t workspace_bytes,
                               float *out, float *softmax_max, float *softmax_sum, void *stream);
 
+/*
+ * li_rope, li_rope_grad -- rotary positions: the rotation that gives q_rope / k_rope of
+ * li_sparse_attention and li_kl_grad (and the rotated part of the indexer's q and k) their
+ * positions, and its gradient. [reading] The pages take the rotated parts as inputs
+ * (aclnnSparseFlashAttentionGrad: queryRope, keyRope; torch_npu.npu_sparse_lightning_indexer_grad_
+ * kl_loss: query_rope, key_rope) and name no rotation; this is the usual one. For a row at
+ * position p and pair i < rope_dim / 2 of every head, with angle a = p freq[i] and magnitude m:
+ *     y[u] = m (x[u] cos a - x[v] sin a),    y[v] = m (x[u] sin a + x[v] cos a)
+ * where (u, v) = (2 i, 2 i + 1) when interleaved = 1 and (i, i + rope_dim / 2) when it is 0, both
+ * counted from rope_offset; the head's other elements are copied. li_rope_grad takes dy in x and
+ * writes dx to y: the transposed map (sin a with the other sign), the other elements copied.
+ *
+ *   x, y       [rows][heads][head_dim] of one dtype (BF16, FP16 or FP32); element (r, h, d) at
+ *              r row_stride + h head_stride + d (strides in elements). y may be x with the same
+ *              strides (in place: only the rotated part is touched); otherwise the elements of y
+ *              must be distinct and must not overlap those of x.
+ *   positions  [rows] int32 or int64 (position_bits 32 or 64), any sign
+ *   freq       radians per position of each pair, in double (li_rope_frequencies fills them);
+ *              angles are reduced in double, so far positions keep their fp32 accuracy
+ * Limits: rope_dim even in [2, 256], 0 <= rope_offset <= head_dim - rope_dim, head_dim <= 4096,
+ * heads in [1, 1024], rows <= 2^31-1. Pointers are aligned to their element. 16-byte aligned data
+ * (pointers, strides, rope_offset; in the half layout also rope_dim / 2) moves in 16-byte
+ * accesses, other data element by element. Products and sums in fp32, one rounding at the end.
+ * Stream-ordered, no allocation, graph-capturable, deterministic.
+ */
+#define LI_ROPE_MAX_PAIRS 128
+typedef struct li_rope_args {
+    const void *x;
+    void *y;
+    const void *positions;
+    int64_t rows;
+    int64_t x_row_stride, x_head_stride, y_row_stride, y_head_stride;
+    int32_t heads, head_dim, rope_dim, rope_offset;
+    int32_t interleaved;                    /* 1: pairs (2i, 2i+1); 0: pairs (i, i + rope_dim/2) */
+    int32_t dtype;                          /* li_dtype of x and y                               */
+    int32_t position_bits;                  /* 32 or 64                                          */
+    float magnitude;                        /* m; 1 unless the frequencies' scaling asks for more */
+    double freq[LI_ROPE_MAX_PAIRS];         /* the first rope_dim / 2 are used                   */
+} li_rope_args;
+li_status li_rope(const li_rope_args *args, void *stream);
+li_status li_rope_grad(const li_rope_args *args, void *stream);
+
+/*
+ * li_rope_frequencies -- the frequencies and the magnitude of a rotation, on the host (no device
+ * is touched). With f_i = base^(-2 i / rope_dim):
+ *   LI_ROPE_PLAIN   freq = f, magnitude 1
+ *   LI_ROPE_LINEAR  freq = f / factor (positions interpolated), magnitude 1
+ *   LI_ROPE_YARN    freq = f (1 - r) + f / factor r, r = clamp((i - low) / max(high - low, 0.001),
+ *                   0, 1), low = max(floor(t(beta_fast)), 0), high = min(ceil(t(beta_slow)),
+ *                   rope_dim - 1), t(n) = rope_dim ln(original_max / (2 pi n)) / (2 ln base): pairs
+ *                   that turn more than beta_fast times over original_max positions keep f, pairs
+ *                   below beta_slow turns are interpolated; magnitude = magnitude_coef ln(factor)
+ *                   + 1 for factor > 1, else 1
+ * freq receives rope_dim / 2 values.
+ */
+typedef enum li_rope_mode { LI_ROPE_PLAIN = 0, LI_ROPE_LINEAR = 1, LI_ROPE_YARN = 2 } li_rope_mode;
+typedef struct li_rope_scaling {
+    double base;                            /* > 1                                               */
+    double factor;                          /* > 0; unused for LI_ROPE_PLAIN                     */
+    double beta_fast, beta_slow;            /* YARN: beta_fast >= beta_slow > 0                  */
+    double magnitude_coef;                  /* YARN: >= 0                                        */
+    int32_t original_max;                   /* YARN: positions the model was trained on, >= 1    */
+    int32_t mode;                           /* li_rope_mode                                      */
+    int32_t rope_dim;
+    int32_t reserved;                       /* must be 0                                         */
+} li_rope_scaling;
+li_status li_rope_frequencies(const li_rope_scaling *scaling, double *freq, float *magnitude);
+
+/*
+ * li_cache_write, li_cache_read -- a key cache in 8 bits: rows quantised as they are written, and
+ * read back. The cache is what li_indexer takes as fp8 keys (k, k_descale) and
+ * li_cache_attention as its keys: E4M3 codes, one fp32 scale per row, and an optional part kept
+ * in the rows' own type (the rope dims). [reading] lightning_indexer, "Prototype": block_table
+ * and the paged cache; aclnnLightningIndexerV2: k_descale; the pages name no writer.
+ *     scale s = max(max_d |x_d| / 448, 2^-90), 1 for a row of zeros; with pow2 = 1 the smallest
+ *     power of two >= max_d |x_d| / 448 (and 2^-90) instead;   code_d = E4M3(x_d / s)
+ * rounded to nearest (ties to even) from the exact quotient. The maximum is taken over the finite
+ * elements; NaN and infinities become the NaN code. li_cache_read gives code x s in fp32, rounded
+ * once to dtype; the rope part is copied.
+ *
+ * E4M3 is a floating format: one scale per row only places its range (2^-9 .. 448), and elements
+ * down to 2^-15 of the row's largest keep their 4 significant bits, so finer scales would add
+ * little.
+ *
+ *   x, rope      rows of the call: [batch][x_len] (layout_x = BSND) at batch b_stride + row_stride,
+ *                or [x_len] (TND, with cu_seqlens [B+1]) at row_stride; dim and rope_dim elements
+ *                of dtype (BF16, FP16 or FP32) each. Read by the write, written by the read.
+ *   codes        layout_k = PA_BSND: (num_blocks, block_size, 1, dim); BSND: (B, k_len, 1, dim)
+ *   descale      fp32 (num_blocks, block_size) or (B, k_len)
+ *   rope_cache   dtype, (num_blocks, block_size, 1, rope_dim) or (B, k_len, 1, rope_dim)
+ *   seqused      [B] or NULL: rows in use per batch (else all of them)
+ *   seqused_k    [B]: keys of each batch, the rows of the call among them; required for PA_BSND,
+ *                k_len when NULL
+ *   block_table  [B][block_table_stride], PA_BSND
+ * Row i of batch b is key position seqused_k[b] - rows_b + i, rows_b its rows in use: the rows of
+ * a call are the last keys of their sequence, as in li_indexer's right-down window.
+ * Rows past rows_b (and TND rows behind the last sequence) are left as they are, in the cache and
+ * in x. Two rows written to one cache row (a block that appears twice) leave it unspecified.
+ *   device_status  uint32 or NULL: LI_DEVERR_LENGTHS is OR-ed in for lengths that do not fit (the
+ *                positions outside the sequence are skipped), LI_DEVERR_TABLE for a block-table
+ *                entry outside [0, num_blocks) (the row is skipped). Read it with
+ *                li_check_status(device_status, stream, &bits).
+ * Limits: dim a multiple of 16 in [16, 1024], rope_dim a multiple of 8 in [0, 256], block_size in
+ * [1, 1024], at most 2^31-1 rows and cache rows; codes 16-byte aligned, descale and indices
+ * 4-byte, rope_cache 16-byte, x and rope aligned to their element (16-byte aligned rows move in
+ * 16-byte accesses). Stream-ordered, no allocation, graph-capturable, deterministic.
+ */
+typedef struct li_cache_args {
+    void *x, *rope;
+    void *codes;
+    float *descale;
+    void *rope_cache;
+    const int32_t *cu_seqlens, *seqused, *seqused_k, *block_table;
+    uint32_t *device_status;
+    int64_t x_batch_stride, x_row_stride, rope_batch_stride, rope_row_stride;   /* elements        */
+    int64_t block_table_stride;
+    int32_t batch, x_len, k_len;            /* x_len: S1 (BSND) or T1 (TND); k_len: BSND cache    */
+    int32_t num_blocks, block_size;         /* PA_BSND                                            */
+    int32_t dim, rope_dim;
+    int32_t layout_x, layout_k;             /* BSND or TND; BSND or PA_BSND                       */
+    int32_t dtype;
+    int32_t pow2;                           /* li_cache_write: power-of-two scales                */
+    int32_t reserved;                       /* must be 0                                          */
+} li_cache_args;
+li_status li_cache_write(const li_cache_args *args, void *stream);
+li_status li_cache_read(const li_cache_args *args, void *stream);
+
 /* Message of the last failing call on this host thread ("" if none). */
 const char *li_last_error_string(void);
 

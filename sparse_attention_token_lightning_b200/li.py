@@ -4,8 +4,9 @@ Argument marshalling only: every step of the indexer runs in the library's CUDA 
 functions keep the C names (``li_metadata``, ``li_indexer``, ``li_merge_topk``, ``li_kl_grad``,
 ...). ``indexer()``, ``merge_topk()`` and ``kl_grad()`` are conveniences that allocate outputs and
 workspaces with torch and call the library on the current stream; ``HostPipeline`` runs the
-indexer over host-resident problems with the copies overlapping the kernels. There is no
-fallback: if the library is missing, loading raises.
+indexer over host-resident problems with the copies overlapping the kernels. ``rope()`` /
+``rope_grad()`` rotate queries and keys, ``cache_write()`` / ``cache_read()`` keep keys as E4M3
+codes with a scale per row. There is no fallback: if the library is missing, loading raises.
 """
 from __future__ import annotations
 
@@ -69,7 +70,8 @@ EXPORTS = ("li_metadata_workspace_size", "li_metadata", "li_indexer_workspace_si
            "li_indexer", "li_check_status", "li_set_stage_events", "li_last_error_string",
            "li_abi_version", "li_indexer_noalloc", "li_plan", "li_merge_topk",
            "li_kl_grad_workspace_size", "li_kl_grad", "li_sparse_attention_workspace_size",
-           "li_sparse_attention")
+           "li_sparse_attention", "li_rope", "li_rope_grad", "li_rope_frequencies",
+           "li_cache_write", "li_cache_read")
 
 MERGE_MAX_LISTS = 16          # LI_MERGE_MAX_LISTS
 
@@ -109,6 +111,52 @@ class LiMergeArgs(ctypes.Structure):
         ("idx_out", ctypes.c_void_p), ("val_out", ctypes.c_void_p),
         ("device_status", ctypes.c_void_p), ("rows", ctypes.c_int64), ("n_lists", ctypes.c_int32),
         ("topk_in", ctypes.c_int32), ("topk_out", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+ROPE_MAX_PAIRS = 128          # LI_ROPE_MAX_PAIRS
+ROPE_MODES = {None: 0, "linear": 1, "yarn": 2}                      # li_rope_mode
+_RopeFreqs = ctypes.c_double * ROPE_MAX_PAIRS
+
+
+class LiRopeArgs(ctypes.Structure):
+    """Mirror of li_rope_args (include/li.h)."""
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("rows", ctypes.c_int64), ("x_row_stride", ctypes.c_int64),
+        ("x_head_stride", ctypes.c_int64), ("y_row_stride", ctypes.c_int64),
+        ("y_head_stride", ctypes.c_int64), ("heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+        ("rope_offset", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("position_bits", ctypes.c_int32),
+        ("magnitude", ctypes.c_float), ("freq", _RopeFreqs),
+    ]
+
+
+class LiRopeScaling(ctypes.Structure):
+    """Mirror of li_rope_scaling (include/li.h)."""
+    _fields_ = [
+        ("base", ctypes.c_double), ("factor", ctypes.c_double), ("beta_fast", ctypes.c_double),
+        ("beta_slow", ctypes.c_double), ("magnitude_coef", ctypes.c_double),
+        ("original_max", ctypes.c_int32), ("mode", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class LiCacheArgs(ctypes.Structure):
+    """Mirror of li_cache_args (include/li.h)."""
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("rope", ctypes.c_void_p), ("codes", ctypes.c_void_p),
+        ("descale", ctypes.c_void_p), ("rope_cache", ctypes.c_void_p),
+        ("cu_seqlens", ctypes.c_void_p), ("seqused", ctypes.c_void_p),
+        ("seqused_k", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+        ("device_status", ctypes.c_void_p), ("x_batch_stride", ctypes.c_int64),
+        ("x_row_stride", ctypes.c_int64), ("rope_batch_stride", ctypes.c_int64),
+        ("rope_row_stride", ctypes.c_int64), ("block_table_stride", ctypes.c_int64),
+        ("batch", ctypes.c_int32), ("x_len", ctypes.c_int32), ("k_len", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32), ("dim", ctypes.c_int32),
+        ("rope_dim", ctypes.c_int32), ("layout_x", ctypes.c_int32), ("layout_k", ctypes.c_int32),
+        ("dtype", ctypes.c_int32), ("pow2", ctypes.c_int32), ("reserved", ctypes.c_int32),
     ]
 
 
@@ -161,6 +209,14 @@ def load(path) -> ctypes.CDLL:
     L.li_sparse_attention.restype = ctypes.c_int
     L.li_merge_topk.argtypes = [ctypes.POINTER(LiMergeArgs), vp]
     L.li_merge_topk.restype = ctypes.c_int
+    L.li_rope.argtypes = [ctypes.POINTER(LiRopeArgs), vp]
+    L.li_rope_grad.argtypes = [ctypes.POINTER(LiRopeArgs), vp]
+    L.li_rope_frequencies.argtypes = [ctypes.POINTER(LiRopeScaling), ctypes.POINTER(ctypes.c_double),
+                                      ctypes.POINTER(ctypes.c_float)]
+    L.li_cache_write.argtypes = [ctypes.POINTER(LiCacheArgs), vp]
+    L.li_cache_read.argtypes = [ctypes.POINTER(LiCacheArgs), vp]
+    for f in ("li_rope", "li_rope_grad", "li_rope_frequencies", "li_cache_write", "li_cache_read"):
+        getattr(L, f).restype = ctypes.c_int
     L.li_abi_version.argtypes = []
     L.li_abi_version.restype = ctypes.c_int32
     return L
@@ -418,6 +474,262 @@ def sparse_attention(ap, stream=None, check: bool = True):
         if st != LI_OK:
             raise LiError(st, f"{li_last_error_string()} (device bits 0x{bits:x})")
     return out, smax, ssum
+
+
+# ---- rotary positions and the quantised key cache ------------------------------------------------
+
+def _on_device(call, args, dev, stream):
+    """call(args, stream) with `dev` current: on `stream`, or on the device's current stream."""
+    handle = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None
+              else stream.cuda_stream)
+    if dev.index == torch.cuda.current_device():
+        _check(call(ctypes.byref(args), handle or None))
+        return
+    with torch.cuda.device(dev):
+        _check(call(ctypes.byref(args), handle or None))
+
+
+def _empty(like, shape, dtype, stream):
+    """An output of a call on `stream` (None: the current one), allocated on that stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _cuda(t, dev, name, dtype=None, shape=None):
+    """`t` is a CUDA tensor on `dev`, of the given type and shape where they are given."""
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}, got one on {t.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _contiguous(t, dev, name, dtype=None, shape=None):
+    _cuda(t, dev, name, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _row_stride(t, lead, name):
+    """(rows, stride) of the first `lead` dimensions taken as one, e.g. (B, S) of (B, S, N, D)."""
+    shape, strides = t.shape, t.stride()
+    rows, step = 1, 0
+    for n, s in zip(reversed(shape[:lead]), reversed(strides[:lead])):
+        if n != 1:
+            if rows == 1:
+                step = s
+            elif s != rows * step and rows:
+                raise ValueError(f"the leading dimensions of {name} must flatten to one stride")
+            rows *= n
+    return rows, step
+
+
+class RopeFrequencies:
+    """Frequencies (radians per position) and magnitude of a rotation of rope_dim elements."""
+
+    __slots__ = ("rope_dim", "magnitude", "freq")
+
+    def __init__(self, rope_dim: int, freq, magnitude: float = 1.0):
+        if rope_dim % 2 or not 2 <= rope_dim <= 2 * ROPE_MAX_PAIRS or len(freq) < rope_dim // 2:
+            raise ValueError(f"rope_dim={rope_dim} with {len(freq)} frequencies")
+        self.rope_dim = int(rope_dim)
+        self.magnitude = float(magnitude)
+        self.freq = freq if isinstance(freq, _RopeFreqs) else _RopeFreqs(*[float(f) for f in freq])
+
+
+def rope_frequencies(rope_dim: int, base: float = 10000.0, scaling: str | None = None,
+                     factor: float = 1.0, original_max: int = 4096, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, magnitude_coef: float = 0.1) -> RopeFrequencies:
+    """li_rope_frequencies: base^(-2 i / rope_dim), plain (scaling None), interpolated ("linear")
+    or "yarn". Host only. Other frequencies: RopeFrequencies(rope_dim, values, magnitude)."""
+    if scaling not in ROPE_MODES:
+        raise ValueError(f"scaling must be one of {list(ROPE_MODES)}, got {scaling!r}")
+    s = LiRopeScaling(base, factor, beta_fast, beta_slow, magnitude_coef, original_max,
+                      ROPE_MODES[scaling], rope_dim, 0)
+    freq, mag = _RopeFreqs(), ctypes.c_float(1.0)
+    _check(lib().li_rope_frequencies(ctypes.byref(s), freq, ctypes.byref(mag)))
+    return RopeFrequencies(rope_dim, freq, mag.value)
+
+
+def _rope(call, x, positions, freqs, offset, interleaved, out, stream):
+    if x.dim() < 2:
+        raise ValueError("x must be (..., heads, head_dim)")
+    dev, lead = x.device, x.dim() - 2
+    _cuda(x, dev, "x")
+    if x.dtype not in DTYPES or x.dtype == torch.float8_e4m3fn:
+        raise ValueError(f"x must be bf16, fp16 or fp32, got {x.dtype}")
+    if x.shape[-1] > 1 and x.stride(-1) != 1:
+        raise ValueError("the last dimension of x must be dense")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"positions must be int32 or int64, got {positions.dtype}")
+    pos = _contiguous(positions, dev, "positions", shape=x.shape[:lead])
+    rows, x_row = _row_stride(x, lead, "x")
+    if out is None:
+        out = _empty(x, x.shape, x.dtype, stream)
+    elif out is not x:
+        _cuda(out, dev, "out", x.dtype, x.shape)
+        if out.shape[-1] > 1 and out.stride(-1) != 1:
+            raise ValueError("the last dimension of out must be dense")
+    _, y_row = _row_stride(out, lead, "out")
+    heads, dim = x.shape[-2:]
+    a = LiRopeArgs(x.data_ptr(), out.data_ptr(), pos, rows, x_row, x.stride(-2), y_row,
+                   out.stride(-2), heads, dim, freqs.rope_dim, offset, int(bool(interleaved)),
+                   DTYPES[x.dtype], 64 if positions.dtype == torch.int64 else 32,
+                   freqs.magnitude, freqs.freq)
+    _on_device(call, a, dev, stream)
+    return out
+
+
+def rope(x, positions, freqs: RopeFrequencies, offset: int = 0, interleaved: bool = False,
+         out=None, stream=None):
+    """Rotary positions (li_rope) of x (..., heads, head_dim), bf16, fp16 or fp32, at positions
+    (...), int32 or int64: elements [offset, offset + freqs.rope_dim) of every head are rotated,
+    the others copied. `out` may be x (in place). Leading dimensions and heads may be strided."""
+    return _rope(lib().li_rope, x, positions, freqs, offset, interleaved, out, stream)
+
+
+def rope_grad(dy, positions, freqs: RopeFrequencies, offset: int = 0, interleaved: bool = False,
+              out=None, stream=None):
+    """The gradient of rope() with respect to its x for the gradient dy of its output
+    (li_rope_grad); same arguments."""
+    return _rope(lib().li_rope_grad, dy, positions, freqs, offset, interleaved, out, stream)
+
+
+def _no_head(t, dims, name):
+    """(..., 1, D) seen as (..., D): keys have one head."""
+    if t.dim() == dims + 1 and t.shape[-2] == 1:
+        return t.squeeze(-2)
+    if t.dim() != dims:
+        raise ValueError(f"{name} has {t.dim()} dimensions, {dims} (or one head more) wanted")
+    return t
+
+
+def _rows_arg(t, dims, name):
+    """Batch and row stride of rows (B, S, D) or (T, D)."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be dense")
+    st = t.stride()
+    return (st[0] if dims == 3 else 0), st[-2]
+
+
+def make_cache_args(x, codes, descale, rope=None, rope_cache=None, seqused_k=None,
+                    block_table=None, cu_seqlens=None, seqused=None, pow2=False,
+                    device_status=None) -> LiCacheArgs:
+    """li_cache_args of device tensors (see cache_write)."""
+    dev = x.device
+    _cuda(x, dev, "x")
+    if x.dtype not in DTYPES or x.dtype == torch.float8_e4m3fn:
+        raise ValueError(f"x must be bf16, fp16 or fp32, got {x.dtype}")
+    if (rope is None) != (rope_cache is None):
+        raise ValueError("rope and rope_cache go together")
+    tnd = cu_seqlens is not None
+    dims = 2 if tnd else 3
+    x = _no_head(x, dims, "x")
+    D = x.shape[-1]
+    a = LiCacheArgs()
+    a.x = x.data_ptr()
+    a.x_batch_stride, a.x_row_stride = _rows_arg(x, dims, "x")
+    rows = x.shape[:-1]
+    if tnd:
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            raise ValueError("cu_seqlens must have shape (B + 1,)")
+        a.cu_seqlens = _contiguous(cu_seqlens, dev, "cu_seqlens", torch.int32)
+        B = cu_seqlens.shape[0] - 1
+        a.layout_x, a.x_len = LAYOUTS["TND"], rows[0]
+    else:
+        B = rows[0]
+        a.layout_x, a.x_len = LAYOUTS["BSND"], rows[1]
+    a.batch = B
+    codes = _no_head(codes, 3, "codes")
+    grid = codes.shape[:2]
+    a.codes = _contiguous(codes, dev, "codes", torch.float8_e4m3fn, (*grid, D))
+    a.descale = _contiguous(descale, dev, "descale", torch.float32, grid)
+    a.dim, a.dtype, a.pow2 = D, DTYPES[x.dtype], int(bool(pow2))
+    if block_table is not None:
+        a.layout_k = LAYOUTS["PA_BSND"]
+        a.num_blocks, a.block_size = grid
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError(f"block_table must be ({B}, blocks), got {tuple(block_table.shape)}")
+        a.block_table = _contiguous(block_table, dev, "block_table", torch.int32)
+        a.block_table_stride = block_table.shape[1]
+    else:
+        if grid[0] != B:
+            raise ValueError(f"a dense cache of {grid[0]} batches, {B} wanted")
+        a.layout_k, a.k_len = LAYOUTS["BSND"], grid[1]
+    if seqused is not None:
+        a.seqused = _contiguous(seqused, dev, "seqused", torch.int32, (B,))
+    if seqused_k is not None:
+        a.seqused_k = _contiguous(seqused_k, dev, "seqused_k", torch.int32, (B,))
+    if rope is not None:
+        rope = _no_head(rope, dims, "rope")
+        R = rope.shape[-1]
+        _cuda(rope, dev, "rope", x.dtype, (*rows, R))
+        a.rope = rope.data_ptr()
+        a.rope_batch_stride, a.rope_row_stride = _rows_arg(rope, dims, "rope")
+        a.rope_cache = _contiguous(_no_head(rope_cache, 3, "rope_cache"), dev, "rope_cache",
+                                   x.dtype, (*grid, R))
+        a.rope_dim = R
+    if device_status is not None:
+        if device_status.element_size() != 4:
+            raise ValueError("device_status must be a 4-byte tensor")
+        a.device_status = _contiguous(device_status, dev, "device_status")
+    return a
+
+
+def _checked(call, a, dev, stream, device_status, check):
+    """Runs a call whose args have a device_status; with check, raises on its bits."""
+    own = check and device_status is None
+    if own:
+        device_status = _empty_status(dev, stream)
+        a.device_status = device_status.data_ptr()
+    _on_device(call, a, dev, stream)
+    if check:
+        with torch.cuda.device(dev):
+            st, bits = li_check_status(device_status, stream)
+        if st != LI_OK:
+            raise LiError(st, f"{li_last_error_string()} (device bits 0x{bits:x})")
+
+
+def _empty_status(dev, stream):
+    if stream is None:
+        return torch.zeros(1, dtype=torch.int32, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.zeros(1, dtype=torch.int32, device=dev)
+
+
+def cache_write(x, codes, descale, rope=None, rope_cache=None, seqused_k=None, block_table=None,
+                cu_seqlens=None, seqused=None, pow2: bool = False, device_status=None, stream=None,
+                check: bool = True):
+    """Quantise key rows into an E4M3 cache (li_cache_write).
+
+    x (B, S, D), or (T, D) with cu_seqlens (B + 1,), bf16 / fp16 / fp32, rows may be strided (a
+    head dimension of 1 before D is taken too); codes float8_e4m3fn and descale fp32, paged
+    (num_blocks, block_size, 1, D) / (num_blocks, block_size) with block_table (B, width) and
+    seqused_k (B,), or dense (B, S2, 1, D) / (B, S2). Row i of batch b is key position
+    seqused_k[b] - rows_b + i, rows_b = seqused[b] (all rows when None). rope / rope_cache: a part
+    of each row kept in its own type. pow2: power-of-two scales. The cache is li_indexer's
+    (k, k_descale) as it stands; with block_table None and (1, rows, D) tensors the call quantises
+    rows in place of a cache, e.g. the indexer's q into codes and q_descale."""
+    a = make_cache_args(x, codes, descale, rope, rope_cache, seqused_k, block_table, cu_seqlens,
+                        seqused, pow2, device_status)
+    _checked(lib().li_cache_write, a, x.device, stream, device_status, check)
+
+
+def cache_read(codes, descale, out, rope_cache=None, rope_out=None, seqused_k=None,
+               block_table=None, cu_seqlens=None, seqused=None, device_status=None, stream=None,
+               check: bool = True):
+    """Rows of an E4M3 cache back as bf16 / fp16 / fp32 (li_cache_read): the arguments of
+    cache_write with `out` (and rope_out) in the place of x (and rope). Reads the last rows_b keys
+    of each batch; seqused = seqused_k reads every key. Rows past rows_b keep what they held.
+    Returns (out, rope_out)."""
+    a = make_cache_args(out, codes, descale, rope_out, rope_cache, seqused_k, block_table,
+                        cu_seqlens, seqused, False, device_status)
+    _checked(lib().li_cache_read, a, out.device, stream, device_status, check)
+    return out, rope_out
 
 
 class HostPipeline:
