@@ -541,6 +541,57 @@ typedef struct li_cache_args {
 li_status li_cache_write(const li_cache_args *args, void *stream);
 li_status li_cache_read(const li_cache_args *args, void *stream);
 
+/*
+ * li_cache_attention -- li_sparse_attention over the E4M3 cache that li_cache_write fills: attention
+ * of every query row over the keys the indexer selected for it, serving single tokens as well as
+ * prefills. For query row r of batch b, head g and the row's selected keys s, with key
+ * k_s = code_s descale_s:
+ *     x[s]     = scale * (q[r,g,:] . k_s + q_rope[r,g,:] . k_rope_s)
+ *     o[r,g,:] = sum_s exp(x[s] - m) k_s / l,   m = max_s x[s],   l = sum_s exp(x[s] - m)
+ * [reading] as li_sparse_attention (aclnnSparseFlashAttentionGrad, calculation formula; value =
+ * key), with the cache's scales (aclnnLightningIndexerV2: k_descale).
+ *
+ * q (B,S1,G,Dm) and q_rope (B,S1,G,Dr) bf16; codes E4M3 (num_blocks,block_size,1,Dm) with
+ * descale fp32 (num_blocks,block_size) and k_rope bf16 (num_blocks,block_size,1,Dr), read through
+ * block_table for layout_k = PA_BSND, or (B,S2,1,Dm), (B,S2) and (B,S2,1,Dr) for BSND.
+ * sparse_indices (B,S1,1,topk) int32, positions in the row's batch, any order; a negative entry
+ * selects nothing, entries may repeat (each counts). Entries >= S2 select nothing and set
+ * LI_DEVERR_LENGTHS, block-table entries outside [0, num_blocks) LI_DEVERR_TABLE, scales outside
+ * [2^-100, 2^100] LI_DEVERR_DESCALE (OR-ed into device_status, a uint32 or NULL; read it with
+ * li_check_status(device_status, stream, &bits)).
+ * Outputs: out bf16 (B,S1,G,Dm); softmax_max and softmax_sum fp32 (B,1,S1,G), both or neither NULL.
+ * A row that selects no key gets out = 0, softmax_max = -inf, softmax_sum = 0. A NaN code in a
+ * selected key makes the row's outputs NaN; keys that are not selected are never read.
+ * Limits: G in [1, 128], Dm in {128, 256, 384, 512}, Dr in {0, 64}, topk in [1, 8192], S2 >= 1
+ * when there are rows, scale positive and finite; q, q_rope, codes, k_rope 16-byte aligned, the
+ * rest to their elements.
+ * Numerics: q and the softmax weights enter the products as two E4M3 parts each (8 and 9
+ * significant bits), the codes as they are, sums in fp32; the scores are exact to fp32 rounding,
+ * the weights to 2^-9 relative, the normaliser sums the unrounded weights.
+ * The workspace (li_cache_attention_workspace_size bytes, 256-byte aligned; it depends on the
+ * current device's SM count) holds partial outputs when a few rows are cut between SMs; contents on
+ * entry are ignored, and calls that may overlap need their own. Stream-ordered, no allocation,
+ * graph-capturable, deterministic (bit-identical reruns on one device model).
+ */
+typedef struct li_cache_attn_args {
+    const void *q, *q_rope;                 /* bf16                                               */
+    const void *codes;
+    const float *descale;
+    const void *k_rope;                     /* bf16                                               */
+    const int32_t *sparse_indices, *block_table;
+    uint32_t *device_status;
+    int64_t block_table_stride;             /* PA_BSND: >= ceil(S2 / block_size); else 0          */
+    float scale;
+    int32_t batch, s1, s2;                  /* B, S1 (query rows per batch), S2 (keys per batch)  */
+    int32_t G, Dm, Dr, topk;
+    int32_t layout_k;                       /* LI_LAYOUT_BSND or LI_LAYOUT_PA_BSND                */
+    int32_t num_blocks, block_size;         /* PA_BSND: >= 1 and 1..1024; else 0                  */
+    int32_t reserved;                       /* must be 0                                          */
+} li_cache_attn_args;
+li_status li_cache_attention_workspace_size(const li_cache_attn_args *args, size_t *bytes);
+li_status li_cache_attention(const li_cache_attn_args *args, void *workspace, size_t workspace_bytes,
+                             void *out, float *softmax_max, float *softmax_sum, void *stream);
+
 /* Message of the last failing call on this host thread ("" if none). */
 const char *li_last_error_string(void);
 

@@ -4,6 +4,7 @@
 #include <initializer_list>
 
 #include "li_cache.cuh"
+#include "li_cache_attn.cuh"
 #include "li_host.cuh"
 #include "li_internal.cuh"
 #include "li_rope.cuh"
@@ -147,6 +148,59 @@ li_status validate_cache_out(const li_cache_args *a) {
     return LI_OK;
 }
 
+li_status validate_cache_attn(const li_cache_attn_args *a, li::CacheAttnPlan *p) {
+    if (!a) return fail(LI_ERR_INVALID_ARG, "args is NULL");
+    if (a->reserved != 0) return fail(LI_ERR_INVALID_ARG, "reserved field must be 0");
+    if (a->batch < 0 || a->s1 < 0 || a->s2 < 0)
+        return fail(LI_ERR_INVALID_ARG, "batch / s1 / s2 must be >= 0");
+    if (a->G < 1 || a->G > 128) return fail(LI_ERR_INVALID_ARG, "G=%d outside [1, 128]", a->G);
+    if (a->Dm < 128 || a->Dm > 512 || a->Dm % 128)
+        return fail(LI_ERR_INVALID_ARG, "Dm=%d must be 128, 256, 384 or 512", a->Dm);
+    if (a->Dr != 0 && a->Dr != 64) return fail(LI_ERR_INVALID_ARG, "Dr=%d must be 0 or 64", a->Dr);
+    if (a->topk < 1 || a->topk > li::kMaxTopk)
+        return fail(LI_ERR_INVALID_ARG, "topk=%d outside [1, 8192]", a->topk);
+    if (!(a->scale > 0.0f) || !(a->scale < 3.0e38f))
+        return fail(LI_ERR_INVALID_ARG, "scale must be a positive finite number");
+    const int64_t rows = (int64_t)a->batch * a->s1;
+    if (rows > 0 && a->s2 < 1) return fail(LI_ERR_INVALID_ARG, "S2=0 with query rows");
+    if (rows > INT32_MAX / 128 || (int64_t)a->batch * a->s2 > INT32_MAX)
+        return fail(LI_ERR_UNSUPPORTED, "more than 2^24-1 query rows or 2^31-1 key rows");
+    if (rows > 0 && (!a->q || !a->codes || !a->descale || !a->sparse_indices))
+        return fail(LI_ERR_INVALID_ARG, "q, codes, descale and sparse_indices are required");
+    if ((a->Dr > 0) != (a->q_rope != nullptr) || (a->Dr > 0) != (a->k_rope != nullptr))
+        return fail(LI_ERR_INVALID_ARG, "q_rope and k_rope go with Dr > 0, and only with it");
+    if (a->layout_k == LI_LAYOUT_PA_BSND) {
+        if (a->block_size < 1 || a->block_size > 1024)
+            return fail(LI_ERR_INVALID_ARG, "block_size=%d outside [1, 1024]", a->block_size);
+        if (a->num_blocks < 1) return fail(LI_ERR_INVALID_ARG, "num_blocks must be >= 1");
+        if ((int64_t)a->num_blocks * a->block_size > INT32_MAX)
+            return fail(LI_ERR_UNSUPPORTED, "more than 2^31-1 cache rows");
+        const int64_t need = ((int64_t)a->s2 + a->block_size - 1) / a->block_size;
+        if (a->block_table_stride < need || a->block_table_stride > INT32_MAX)
+            return fail(LI_ERR_INVALID_ARG, "block_table_stride=%lld outside [ceil(S2 / block_size)=%lld, 2^31-1]",
+                        (long long)a->block_table_stride, (long long)need);
+        if (rows > 0 && !a->block_table)
+            return fail(LI_ERR_INVALID_ARG, "PA_BSND needs a block_table");
+    } else if (a->layout_k == LI_LAYOUT_BSND) {
+        if (a->block_table || a->block_table_stride || a->num_blocks || a->block_size)
+            return fail(LI_ERR_INVALID_ARG, "block_table fields are for PA_BSND only");
+    } else {
+        return fail(LI_ERR_INVALID_ARG, "layout_k=%d must be BSND or PA_BSND", a->layout_k);
+    }
+    if (!aligned(a->q, 16) || !aligned(a->q_rope, 16) || !aligned(a->codes, 16) || !aligned(a->k_rope, 16) ||
+        !aligned(a->descale, 4) || !aligned(a->sparse_indices, 4) || !aligned(a->block_table, 4) ||
+        !aligned(a->device_status, 4))
+        return fail(LI_ERR_INVALID_ARG, "q, codes and the rope parts must be 16-byte aligned, the "
+                    "others 4-byte");
+    if (!li::cache_attn_plan(*a, p))
+        return fail(LI_ERR_UNSUPPORTED, "G=%d with Dm=%d does not fit the kernel's shared memory", a->G, a->Dm);
+    return LI_OK;
+}
+
+size_t cache_attn_bytes(const li::CacheAttnPlan &p) {
+    return li::align_up(p.partial_floats * sizeof(float) + 1, 256);
+}
+
 }  // namespace
 
 extern "C" {
@@ -223,6 +277,34 @@ li_status li_cache_read(const li_cache_args *args, void *stream) {
     if (st != LI_OK) return st;
     cudaError_t e = li::launch_cache_read(*args, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(LI_ERR_CUDA, "cache read launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+li_status li_cache_attention_workspace_size(const li_cache_attn_args *args, size_t *bytes) {
+    li::CacheAttnPlan p;
+    li_status st = validate_cache_attn(args, &p);
+    if (st != LI_OK) return st;
+    if (!bytes) return fail(LI_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = cache_attn_bytes(p);
+    return ok();
+}
+
+li_status li_cache_attention(const li_cache_attn_args *args, void *workspace, size_t workspace_bytes,
+                             void *out, float *softmax_max, float *softmax_sum, void *stream) {
+    NvtxRange range("li_cache_attention");
+    li::CacheAttnPlan p;
+    li_status st = validate_cache_attn(args, &p);
+    if (st != LI_OK) return st;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < cache_attn_bytes(p))
+        return fail(LI_ERR_WORKSPACE, "workspace must be a 256-byte aligned device buffer of >= %zu bytes",
+                    cache_attn_bytes(p));
+    if (p.units == 0) return ok();
+    if (!out || !aligned(out, 16)) return fail(LI_ERR_INVALID_ARG, "out must be a 16-byte aligned device buffer");
+    if ((softmax_max == nullptr) != (softmax_sum == nullptr) || !aligned(softmax_max, 4) || !aligned(softmax_sum, 4))
+        return fail(LI_ERR_INVALID_ARG, "softmax_max and softmax_sum go together, 4-byte aligned");
+    cudaError_t e = li::launch_cache_attention(*args, p, static_cast<float *>(workspace), out, softmax_max,
+                                               softmax_sum, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(LI_ERR_CUDA, "cache attention launch: %s", cudaGetErrorString(e));
     return ok();
 }
 

@@ -1,0 +1,964 @@
+// Attention over the selected rows of an E4M3 key cache (li_cache_attention), sm_100a.
+//
+// Query row r of batch b, head g, selected cache rows s with codes c_s and scale d_s (k_s = d_s c_s):
+//     x[s]   = scale (d_s q.c_s + q_rope.k_rope_s),   o = sum_s e^x[s] d_s c_s / sum_s e^x[s]
+//
+// The codes go to the tensor cores as they lie in the cache: no key is converted. What multiplies
+// them is split into E4M3 parts instead, whose products with the codes and sums in fp32 are exact
+// to fp32 rounding:
+//   q       times a power of two per head (largest element in [128, 256)) = hi + lo / 16, hi and
+//           lo in E4M3: 8 bits in 4 + 4, so every bf16 element down to 2^-13 of the row's largest
+//           is held exactly (and none is off by more than 2^-22 of it)
+//   weights with y = x log2(e) + log2(d_s), 2^(y - ref + 5) = hi + lo / 16 likewise (9 bits, half
+//           the error of a bf16 weight). The reference follows the largest y, not the largest x, so
+//           the scale is inside the exponent and the parts are full where the products are large;
+//           the normaliser sums 2^(y - ref + 5) / d_s in fp32.
+// The products S = K Q^T (keys on M = 128, hi and lo heads on N) and O^T += V^T P^T (dims on M = 128,
+// the key tile read MN-major, keys on K) both read the same gathered tile; the rope part is a bf16
+// product of its own into other TMEM columns, since its codes have no scale.
+//
+// One CTA per SM works on units (row, block of up to 32 heads), whole units in turn when there are
+// many rows, or an equal share of all units' tiles of 128 selected keys when there are few
+// (decode): a unit cut between CTAs leaves partial outputs, which a second kernel joins. Warps:
+//   softmax   4 per 16 heads: a thread owns one key of the tile and 16 heads. The reference moves
+//             only when some y exceeds it by more than 3 (every weight <= 2^8 of the 448 that E4M3
+//             holds); a vote per tile finds that out, the maxima are reduced only then
+//   prep      the next unit's q: normalised, split and stored in the MMA layout
+//   gather    looks up each selected key's cache row, keeps its scale for the softmax warps and
+//             copies codes and rope part with cp.async into 16 KB slots (128 keys x 128 bytes,
+//             128-byte swizzle; rows that select nothing are zero-filled)
+//   scheduler the CTA's units;  qk / pv: one thread each issues the two products
+// Every wait is bounded in time; on expiry the kernel records LI_DEVERR_TIMEOUT and returns. The
+// softmax warps of a group agree on giving up (the vote carries it), so none is left at a barrier.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "li_cache_attn.cuh"
+#include "li_internal.cuh"
+#include "li_sm100.cuh"
+
+namespace li {
+namespace {
+
+using namespace sm100;
+
+constexpr int kKeys = 128;                          // selected keys per tile (MMA M)
+constexpr uint32_t kSlot = kKeys * 128;             // 128 bytes of 128 keys
+constexpr int kMaxSlots = 16, kTileRing = 8, kAhRing = 4;
+constexpr int kGatherWarps = 4;
+constexpr uint32_t kSmemBytes = 232448;
+constexpr uint32_t kTailBytes = 8192;
+constexpr uint32_t kTailOff = kSmemBytes - kTailBytes;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 3.0f;                      // log2 units above the reference
+constexpr float kShift = 5.0f;                      // weights are 2^(y - ref + kShift) <= 2^8
+constexpr float kMinDescale = 7.888609052210118e-31f, kMaxDescale = 1.2676506002282294e30f;  // 2^+-100
+constexpr uint32_t kDevErrInternal = 0x20u;
+
+template <int N> struct Roles {
+    static constexpr int kGroups = N / 16;              // softmax groups of 4 warps, 16 heads each
+    static constexpr int kSoft = 4 * kGroups;
+    static constexpr int kPrep0 = kSoft, kPrep = N == 16 ? 4 : 2;
+    static constexpr int kGather0 = kPrep0 + kPrep;
+    static constexpr int kSched = kGather0 + kGatherWarps, kQk = kSched + 1, kPv = kSched + 2;
+    static constexpr int kThreads = 32 * (kSched + 3);
+};
+
+struct Unit {
+    int32_t row;            // -1: no more units
+    int32_t head0;          // first head
+    int32_t tile0, tiles;   // tiles of the row's selection
+    int32_t part;           // partial slot, or -1: the unit is whole
+};
+
+// Barriers and small arrays in the shared-memory tail.
+struct Bars {
+    uint32_t base;
+    __device__ uint32_t at(int i) const { return base + 8 * i; }
+    __device__ uint32_t u_full(int i) const { return at(0 + i); }
+    __device__ uint32_t u_empty(int i) const { return at(2 + i); }
+    __device__ uint32_t q_full(int i) const { return at(4 + i); }
+    __device__ uint32_t q_empty(int i) const { return at(6 + i); }
+    __device__ uint32_t s_full(int i) const { return at(8 + i); }
+    __device__ uint32_t s_empty(int i) const { return at(10 + i); }
+    __device__ uint32_t p_full(int i) const { return at(12 + i); }
+    __device__ uint32_t p_empty(int i) const { return at(14 + i); }
+    __device__ uint32_t o_done() const { return at(16); }
+    __device__ uint32_t o_empty() const { return at(17); }
+    __device__ uint32_t tile_full(int i) const { return at(18 + i); }
+    __device__ uint32_t meta_full(int i) const { return at(18 + kTileRing + i); }
+    __device__ uint32_t slot_empty(int i) const { return at(18 + 2 * kTileRing + i); }
+};
+constexpr int kNumBars = 18 + 2 * kTileRing + kMaxSlots;
+struct Tail {
+    uint64_t bars[kNumBars];
+    Unit unit[2];
+    uint32_t tmem;
+    volatile int abort_flag;
+    alignas(16) int vote[2][2][4];              // [group][tile parity][warp]
+    alignas(16) float ah[kAhRing][32];          // scale log2(e) / the head's power of two
+    alignas(16) float ref[2][16];               // [group][head]
+    alignas(16) float alpha[2][16];
+    alignas(16) float red[2][16][4];            // [group][head][warp]
+    alignas(16) float lsum[2][16][4], mx[2][16][4];
+    alignas(16) float descale[kTileRing][kKeys];    // 0: the entry selects nothing
+};
+static_assert(sizeof(Tail) <= kTailBytes, "shared memory tail");
+
+struct Params {
+    const uint16_t *q, *q_rope;
+    const uint8_t *codes;
+    const float *descale;
+    const uint16_t *k_rope;
+    const int32_t *indices, *block_table;
+    uint32_t *status;
+    uint16_t *out;
+    float *smax, *ssum;
+    float *part_o, *part_stat;          // [2 grid][N][Dm], [2 grid][N][3]
+    int64_t bt_stride, key_rows;
+    int64_t units;
+    float scale;
+    int32_t rows, s1, s2, G, Dm, topk, block_size, num_blocks;
+    int32_t has_rope, blocks, head_blocks, tiles, split;
+    int32_t q_bufs, slots;
+    uint32_t q_bytes, p_off, slot_off, tmem_cols;
+};
+
+struct Ring {
+    int idx = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++idx == n) { idx = 0; phase ^= 1u; }
+    }
+};
+
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// 16-byte copy, `bytes` (0 or 16) of them read and the rest filled with zeros.
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ float exp2_(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 e4m3x2_f32(uint32_t v) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3);
+    return __half22float2(__half2(h));
+}
+// Largest of v over the warp (NaN counts as -infinity).
+__device__ __forceinline__ float warp_max(float v) {
+    int i = __float_as_int(v == v ? v : -__int_as_float(0x7f800000));
+    i ^= (i >> 31) & 0x7fffffff;
+    i = __reduce_max_sync(0xffffffffu, i);
+    return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+// Sums (or maxima) of 16 values over the warp: lane l returns value 8 (l >> 4) + 4 (l >> 3 & 1) +
+// 2 (l >> 2 & 1) + (l >> 1 & 1), i.e. value l >> 1.
+template <bool kMax>
+__device__ __forceinline__ float transpose_reduce(const float (&v)[16], int lane) {
+    float a[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a[i] = v[i];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const int bit = 16 >> s, half = 8 >> s;
+        const bool up = (lane & bit) != 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < half) {
+                const float keep = up ? a[i + half] : a[i];
+                const float send = up ? a[i] : a[i + half];
+                const float recv = __shfl_xor_sync(0xffffffffu, send, bit);
+                a[i] = kMax ? fmaxf(keep, recv) : keep + recv;
+            }
+    }
+    const float o = __shfl_xor_sync(0xffffffffu, a[0], 1);
+    return kMax ? fmaxf(a[0], o) : a[0] + o;
+}
+
+// First tile of CTA c's share of all units' tiles.
+__host__ __device__ inline int64_t share(int64_t total, int grid, int c) { return total * c / grid; }
+
+// ---- scheduler -----------------------------------------------------------------------------------
+__device__ void scheduler_role(const Params &P, Tail *T, const Bars &bars) {
+    const int lane = threadIdx.x & 31;
+    const int64_t total = P.units * P.tiles;
+    int64_t t = P.split ? share(total, gridDim.x, blockIdx.x) : (int64_t)blockIdx.x * P.tiles;
+    const int64_t end = P.split ? share(total, gridDim.x, blockIdx.x + 1) : total;
+    for (int it = 0;; ++it) {
+        const bool more = t < end;
+        Unit u{-1, 0, 0, 0, -1};
+        if (more) {
+            const int64_t unit = t / P.tiles;
+            u.row = (int32_t)(unit / P.head_blocks);
+            u.head0 = (int32_t)(unit - (int64_t)u.row * P.head_blocks) * 32;
+            u.tile0 = (int32_t)(t - unit * P.tiles);
+            const int64_t left = P.split ? min((int64_t)P.tiles - u.tile0, end - t) : P.tiles;
+            u.tiles = (int32_t)left;
+            if (P.split && u.tiles != P.tiles) u.part = 2 * blockIdx.x + (u.tile0 == 0 ? 1 : 0);
+            t += P.split ? left : (int64_t)gridDim.x * P.tiles;
+            // tiles behind the last selected entry are left out
+            const int32_t *ir = P.indices + (int64_t)u.row * P.topk;
+            const int from = u.tile0 * kKeys, to = min((u.tile0 + u.tiles) * kKeys, P.topk);
+            if (__ldg(ir + to - 1) < 0) {
+                int last = -1;
+#pragma unroll 8
+                for (int p = from + lane; p < to; p += 32)
+                    if (__ldg(ir + p) >= 0) last = p;
+                last = __reduce_max_sync(0xffffffffu, last);
+                u.tiles = last < from ? 0 : (last - from) / kKeys + 1;
+            }
+        }
+        if (!wait_warp(bars.u_empty(it & 1), ((it >> 1) & 1) ^ 1, &T->abort_flag)) {
+            T->abort_flag = 1;
+            return;
+        }
+        if (lane == 0) {
+            T->unit[it & 1] = u;
+            mbar_arrive(bars.u_full(it & 1));
+        }
+        __syncwarp();
+        if (!more) return;
+    }
+}
+
+// The it-th unit of this CTA, taken by a whole warp; false on giving up.
+__device__ __forceinline__ bool take_unit(Tail *T, const Bars &bars, int it, Unit *u) {
+    if (!wait_warp(bars.u_full(it & 1), (it >> 1) & 1, &T->abort_flag)) return false;
+    *u = T->unit[it & 1];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bars.u_empty(it & 1));
+    return true;
+}
+// The same for a role of one thread.
+__device__ __forceinline__ bool take_unit_thread(Tail *T, const Bars &bars, int it, Unit *u) {
+    if (!mbar_wait(bars.u_full(it & 1), (it >> 1) & 1, &T->abort_flag)) return false;
+    *u = T->unit[it & 1];
+    mbar_arrive(bars.u_empty(it & 1));
+    return true;
+}
+
+// ---- q: normalised and split ---------------------------------------------------------------------
+template <int N>
+__device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bars) {
+    using R = Roles<N>;
+    const int wp = (threadIdx.x >> 5) - R::kPrep0, lane = threadIdx.x & 31;
+    const float kInf = __int_as_float(0x7f800000);
+    Ring qr;
+    int n = 0;                                  // units with tiles so far
+    for (int it = 0;; ++it) {
+        Unit u;
+        if (!take_unit(T, bars, it, &u)) break;
+        if (u.row < 0) return;
+        if (u.tiles == 0) continue;
+        if (!wait_warp(bars.q_empty(qr.idx), qr.phase ^ 1u, &T->abort_flag)) break;
+        uint8_t *qb = smem + qr.idx * P.q_bytes;
+        uint8_t *rb = qb + P.blocks * (2 * N * 128);
+        const int heads = min(P.G - u.head0, N);
+        for (int h = wp; h < N; h += R::kPrep) {
+            const bool real = h < heads;
+            const int64_t qrow = (int64_t)u.row * P.G + u.head0 + (real ? h : 0);
+            uint4 v[2];
+            float amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int vec = lane + 32 * i;          // 8 elements
+                v[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (real && vec * 8 < P.Dm && idx_ok(qrow * P.Dm + vec * 8, (int64_t)P.rows * P.G * P.Dm, P.status))
+                    v[i] = __ldg(reinterpret_cast<const uint4 *>(P.q + qrow * P.Dm) + vec);
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float a = fabsf(bf16_lo(w[j])), b = fabsf(bf16_hi(w[j]));
+                    if (a < kInf) amax = fmaxf(amax, a);
+                    if (b < kInf) amax = fmaxf(amax, b);
+                }
+            }
+            amax = warp_max(amax);
+            // f = 2^(7 - exponent of amax): the largest element lands in [128, 256)
+            const int e = max((int)(__float_as_uint(amax) >> 23), 8);   // biased; 8 keeps f finite
+            const float f = amax > 0.0f ? __uint_as_float((uint32_t)(127 + 7 + 127 - e) << 23) : 1.0f;
+            if (lane == 0) T->ah[n & (kAhRing - 1)][h] = P.scale * kLog2e / f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int vec = lane + 32 * i;
+                if (vec * 8 >= P.Dm) continue;
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // an infinity has no code: NaN, so that the head's result shows it
+                    float a = bf16_lo(w[j]) * f, b = bf16_hi(w[j]) * f;
+                    if (!(fabsf(a) < kInf)) a = __int_as_float(0x7fc00000);
+                    if (!(fabsf(b) < kInf)) b = __int_as_float(0x7fc00000);
+                    hi[j] = e4m3x2(a, b);
+                    const float2 r = e4m3x2_f32(hi[j]);
+                    lo[j] = e4m3x2((a - r.x) * 16.0f, (b - r.y) * 16.0f);
+                }
+                const int off = (vec * 8) & 127, b = vec >> 4;
+                const uint32_t at = (uint32_t)(b * 2 * N * 128 + (((off >> 4) ^ (h & 7)) << 4) + (off & 8));
+                *reinterpret_cast<uint2 *>(qb + at + h * 128) =
+                    make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                *reinterpret_cast<uint2 *>(qb + at + (N + h) * 128) =
+                    make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            }
+            if (P.has_rope && lane < 8) {
+                uint4 r = make_uint4(0u, 0u, 0u, 0u);
+                if (real && idx_ok(qrow * 64 + lane * 8, (int64_t)P.rows * P.G * 64, P.status))
+                    r = __ldg(reinterpret_cast<const uint4 *>(P.q_rope + qrow * 64) + lane);
+                *reinterpret_cast<uint4 *>(rb + h * 128 + ((lane ^ (h & 7)) << 4)) = r;
+            }
+        }
+        fence_async_smem();
+        mbar_arrive(bars.q_full(qr.idx));
+        qr.next(P.q_bufs);
+        ++n;
+    }
+    T->abort_flag = 1;
+}
+
+// ---- gather ----------------------------------------------------------------------------------------
+// Cache row and scale of entry pos of the unit's row (-1, 0 where it selects nothing).
+__device__ __forceinline__ void look_up(const Params &P, const int32_t *ir, int64_t b, int pos, int32_t *row,
+                                        float *d, uint32_t *err) {
+    *row = -1;
+    *d = 0.0f;
+    const int32_t v = pos < P.topk ? __ldg(ir + pos) : -1;
+    if (v < 0) return;
+    if (v >= P.s2) {
+        *err |= LI_DEVERR_LENGTHS;
+        return;
+    }
+    int64_t r;
+    if (P.block_table) {
+        const int32_t q = v / P.block_size;
+        const int32_t blk = __ldg(P.block_table + b * P.bt_stride + q);
+        if (blk < 0 || blk >= P.num_blocks) {
+            *err |= LI_DEVERR_TABLE;
+            return;
+        }
+        r = (int64_t)blk * P.block_size + (v - q * P.block_size);
+    } else {
+        r = b * P.s2 + v;
+    }
+    if (!idx_ok(r, P.key_rows, P.status)) return;
+    const float s = __ldg(P.descale + r);
+    if (!(s >= kMinDescale && s <= kMaxDescale)) {
+        *err |= LI_DEVERR_DESCALE;
+        return;
+    }
+    *row = (int32_t)r;
+    *d = s;
+}
+
+template <int N>
+__device__ void gather_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bars) {
+    const int w = (threadIdx.x >> 5) - Roles<N>::kGather0, lane = threadIdx.x & 31;
+    const int piece = lane & 7, sub = lane >> 3;            // this lane copies keys 32 w + sub + 4 i
+    const uint32_t slots = smem_u32(smem) + P.slot_off;
+    const int key0 = 32 * w + sub;
+    // 16-byte piece of row key in a swizzled slot; key & 7 is sub + 4 (i & 1)
+    const uint32_t dst0 = (uint32_t)(key0 * 128 + ((piece ^ sub) << 4));
+    const uint32_t dst1 = (uint32_t)(key0 * 128 + ((piece ^ (sub + 4)) << 4));
+    Ring sr, tr;
+    uint32_t err = 0;
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
+        Unit u;
+        if (!take_unit(T, bars, it, &u)) { ok = false; break; }
+        if (u.row < 0) break;
+        const int32_t *ir = P.indices + (int64_t)u.row * P.topk;
+        const int64_t b = u.row / P.s1;
+        int32_t mine = -1;
+        float d = 0.0f;
+        int pos = u.tile0 * kKeys + 32 * w + lane;
+        if (u.tiles > 0) look_up(P, ir, b, pos, &mine, &d, &err);
+        for (int j = 0; j < u.tiles && ok; ++j, tr.next(kTileRing)) {
+            T->descale[tr.idx][32 * w + lane] = d;
+            mbar_arrive(bars.meta_full(tr.idx));
+            int32_t row[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) row[i] = __shfl_sync(0xffffffffu, mine, sub + 4 * i);
+            if (P.has_rope) {
+                if (!wait_warp(bars.slot_empty(sr.idx), sr.phase ^ 1u, &T->abort_flag)) { ok = false; break; }
+                const uint32_t base = slots + sr.idx * kSlot;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int64_t r = row[i] < 0 ? 0 : row[i];
+                    cp_async16_zfill(base + i * 512 + (i & 1 ? dst1 : dst0), P.k_rope + r * 64 + piece * 8,
+                                     row[i] < 0 ? 0u : 16u);
+                }
+                sr.next(P.slots);
+            }
+            for (int c = 0; c < P.blocks; ++c, sr.next(P.slots)) {
+                if (!wait_warp(bars.slot_empty(sr.idx), sr.phase ^ 1u, &T->abort_flag)) { ok = false; break; }
+                const uint32_t base = slots + sr.idx * kSlot;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int64_t r = row[i] < 0 ? 0 : row[i];
+                    cp_async16_zfill(base + i * 512 + (i & 1 ? dst1 : dst0),
+                                     P.codes + r * P.Dm + c * 128 + piece * 16, row[i] < 0 ? 0u : 16u);
+                }
+            }
+            if (!ok) break;
+            cp_async_arrive(bars.tile_full(tr.idx));
+            pos += kKeys;
+            if (j + 1 < u.tiles) look_up(P, ir, b, pos, &mine, &d, &err);
+        }
+    }
+    // no copy may still be writing shared memory when the CTA leaves
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ok) T->abort_flag = 1;
+    if (err && P.status) atomicOr(P.status, err);
+}
+
+// ---- products --------------------------------------------------------------------------------------
+// TMEM: S of tile parity p at p kSCols: [0, 2N) hi and lo of q.c, [2N, 3N) the rope product;
+// O block b at 2 kSCols + 2N b: [0, N) hi, [N, 2N) lo.
+template <int N> constexpr uint32_t kSCols = 4 * N;
+
+template <int N>
+__device__ void qk_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bars, uint32_t tmem) {
+    const uint32_t sbase = smem_u32(smem), slots = sbase + P.slot_off;
+    constexpr uint32_t kQBlock = 2 * N * 128;
+    constexpr uint32_t idesc8 = (1u << 4) | ((2u * N >> 3) << 17) | (8u << 24);
+    constexpr uint32_t idesc16 = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+    Ring qr, sr, tr;
+    uint32_t kt = 0;
+    for (int it = 0;; ++it) {
+        Unit u;
+        if (!take_unit_thread(T, bars, it, &u)) break;
+        if (u.row < 0) return;
+        if (u.tiles == 0) continue;
+        if (!mbar_wait(bars.q_full(qr.idx), qr.phase, &T->abort_flag)) break;
+        const uint32_t qa = sbase + qr.idx * P.q_bytes;
+        bool ok = true;
+        for (int j = 0; j < u.tiles; ++j, ++kt, tr.next(kTileRing)) {
+            const uint32_t b = kt & 1u;
+            ok = mbar_wait(bars.s_empty(b), ((kt >> 1) & 1u) ^ 1u, &T->abort_flag) &&
+                 mbar_wait(bars.tile_full(tr.idx), tr.phase, &T->abort_flag);
+            if (!ok) break;
+            fence_async_smem();
+            tc_fence_after();
+            const uint32_t d = tmem + b * kSCols<N>;
+            if (P.has_rope) {
+                const uint64_t a = sw128_desc(slots + sr.idx * kSlot);
+                const uint64_t q = sw128_desc(qa + P.blocks * kQBlock);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma_f16(d + 2 * N, a + 2 * k, q + 2 * k, idesc16, k > 0);
+                umma_commit(bars.slot_empty(sr.idx));
+                sr.next(P.slots);
+            }
+            for (int c = 0; c < P.blocks; ++c, sr.next(P.slots)) {
+                const uint64_t a = sw128_desc(slots + sr.idx * kSlot);
+                const uint64_t q = sw128_desc(qa + c * kQBlock);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma_f8(d, a + 2 * k, q + 2 * k, idesc8, (c | k) != 0);
+            }
+            umma_commit(bars.s_full(b));
+        }
+        if (!ok) break;
+        umma_commit(bars.q_empty(qr.idx));
+        qr.next(P.q_bufs);
+    }
+    T->abort_flag = 1;
+}
+
+template <int N>
+__device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bars, uint32_t tmem) {
+    const uint32_t sbase = smem_u32(smem), slots = sbase + P.slot_off;
+    constexpr uint32_t idesc = (1u << 4) | (1u << 15) | ((2u * N >> 3) << 17) | (8u << 24);
+    Ring sr;
+    uint32_t kt = 0, nu = 0;
+    for (int it = 0;; ++it) {
+        Unit u;
+        if (!take_unit_thread(T, bars, it, &u)) break;
+        if (u.row < 0) return;
+        if (u.tiles == 0) continue;
+        bool ok = true;
+        for (int j = 0; j < u.tiles; ++j, ++kt) {
+            // the unit's first product overwrites O: the unit before must have been read out
+            ok = (j > 0 || nu == 0 || mbar_wait(bars.o_empty(), (nu - 1) & 1u, &T->abort_flag)) &&
+                 mbar_wait(bars.p_full(kt & 1u), (kt >> 1) & 1u, &T->abort_flag);
+            if (!ok) break;
+            fence_async_smem();
+            tc_fence_after();
+            const uint64_t p = sw128_desc(sbase + P.p_off + (kt & 1u) * (2 * N * 128));
+            if (P.has_rope) sr.next(P.slots);
+            for (int c = 0; c < P.blocks; ++c, sr.next(P.slots)) {
+                const uint32_t va = slots + sr.idx * kSlot;
+                const uint32_t d = tmem + 2 * kSCols<N> + c * 2 * N;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    umma_f8(d, sw128_desc_mn(va + k * 32 * 128, kSlot), p + 2 * k, idesc, (j | k) != 0);
+                umma_commit(bars.slot_empty(sr.idx));
+            }
+            umma_commit(bars.p_empty(kt & 1u));
+            umma_commit(bars.o_done());
+        }
+        if (!ok) break;
+        ++nu;
+    }
+    T->abort_flag = 1;
+}
+
+// ---- softmax and output ------------------------------------------------------------------------------
+template <int N>
+__device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bars, uint32_t tmem) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = warp >> 2, q = warp & 3;              // group (16 heads), quarter of the TMEM lanes
+    const int key = 32 * q + lane;                      // key of the tile; dim of an O block
+    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    const float kInf = __int_as_float(0x7f800000);
+    volatile int *abort_flag = &T->abort_flag;
+    const int bar_id = 1 + g;
+    Ring tr;
+    uint32_t kt = 0;
+    int nu = 0;
+    bool ok = true;
+    for (int it = 0;; ++it) {
+        Unit u;
+        // the group's warps agree on giving up here too (a vote below carries a failure on)
+        bool got = mbar_wait(bars.u_full(it & 1), (it >> 1) & 1, abort_flag);
+        got = __all_sync(0xffffffffu, got) && ok;
+        if (lane == 0) T->vote[g][kt & 1][q] = got ? 0 : 2;
+        named_bar(bar_id, 128);
+        {
+            const int4 v = *reinterpret_cast<const int4 *>(T->vote[g][kt & 1]);
+            if ((v.x | v.y | v.z | v.w) & 2) break;
+        }
+        u = T->unit[it & 1];
+        named_bar(bar_id, 128);                         // the vote slot is written again below
+        if (lane == 0) mbar_arrive(bars.u_empty(it & 1));
+        if (u.row < 0) return;
+        const int heads = min(P.G - u.head0 - 16 * g, 16);      // may be <= 0
+        const int64_t head_at = (int64_t)u.row * P.G + u.head0 + 16 * g;
+        const bool row_ok = idx_ok(u.row, P.rows, P.status);
+        float l[16], mx[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) { l[i] = 0.0f; mx[i] = -kInf; }
+        if (u.tiles > 0 && q == 0 && lane < 16) T->ref[g][lane] = -kInf;
+        if (u.tiles > 0) named_bar(bar_id, 128);
+        bool give_up = false;
+        for (int j = 0; j < u.tiles; ++j, ++kt, tr.next(kTileRing)) {
+            const uint32_t b = kt & 1u;
+            ok = ok && wait_warp(bars.meta_full(tr.idx), tr.phase, abort_flag);
+            const float d = ok ? T->descale[tr.idx][key] : 0.0f;
+            const bool valid = d > 0.0f;
+            const float log2d = valid ? log2f(d) : 0.0f, inv_d = valid ? __frcp_rn(d) : 0.0f;
+            ok = ok && wait_warp(bars.s_full(b), (kt >> 1) & 1u, abort_flag);
+            float y[16];
+            tc_fence_after();
+            {
+                uint32_t hi[16], lo[16];
+                const uint32_t s = tmem + lanes + b * kSCols<N> + 16 * g;
+                tmem_ld16_nowait(s, hi);
+                tmem_ld16_nowait(s + N, lo);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    y[i] = d * fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
+                const float *ah = T->ah[nu & (kAhRing - 1)] + 16 * g;
+                if (P.has_rope) {
+                    tmem_ld16_nowait(s + 2 * N, hi);
+                    tmem_wait_ld();
+                    const float rs = P.scale * kLog2e;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) y[i] = fmaf(y[i], ah[i], rs * __uint_as_float(hi[i]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) y[i] *= ah[i];
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.s_empty(b));
+            bool over = false;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (valid) mx[i] = fmaxf(mx[i], y[i]);
+                y[i] = valid ? y[i] + log2d : -kInf;
+                over |= y[i] > T->ref[g][i] + kSlack;
+            }
+            const bool any = __any_sync(0xffffffffu, over);
+            if (lane == 0) T->vote[g][b][q] = (any ? 1 : 0) | (ok ? 0 : 2);
+            named_bar(bar_id, 128);
+            const int4 v4 = *reinterpret_cast<const int4 *>(T->vote[g][b]);
+            const int v = v4.x | v4.y | v4.z | v4.w;
+            if (v & 2) { give_up = true; break; }
+            if (v & 1) {
+                // the references move to the tile's maxima; O and the sums follow
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float m = warp_max(y[i]);
+                    if (lane == 0) T->red[g][i][q] = m;
+                }
+                named_bar(bar_id, 128);
+                if (q == 0 && lane < 16) {
+                    const float4 m4 = *reinterpret_cast<const float4 *>(T->red[g][lane]);
+                    const float old = T->ref[g][lane];
+                    const float m = fmaxf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), old);
+                    T->ref[g][lane] = m;
+                    T->alpha[g][lane] = old > -kInf ? exp2_(old - m) : (m > -kInf ? 0.0f : 1.0f);
+                }
+                named_bar(bar_id, 128);
+                float al[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    al[i] = T->alpha[g][i];
+                    l[i] *= al[i];
+                }
+                if (j > 0) {
+                    ok = ok && wait_warp(bars.o_done(), (kt - 1) & 1u, abort_flag);
+                    tc_fence_after();
+                    for (int c = 0; c < 2 * P.blocks; ++c) {
+                        const uint32_t o = tmem + lanes + 2 * kSCols<N> + c * N + 16 * g;
+                        float t[16];
+                        tmem_ld16(o, t);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) t[i] *= al[i];
+                        tmem_st16(o, t);
+                    }
+                    tc_fence_before();
+                }
+            }
+            ok = ok && wait_warp(bars.p_empty(b), ((kt >> 1) & 1u) ^ 1u, abort_flag);
+            // weights as hi + lo / 16; rows of the MMA operand: head (hi), N + head (lo)
+            uint8_t *pb = smem + P.p_off + b * (2 * N * 128) + 16 * g * 128 + (key & 15);
+            const uint32_t kc = (uint32_t)(key >> 4) << 4;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                float p[2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    // a reference of -infinity is met only by y = -infinity: weight 0
+                    const float r = fmaxf(T->ref[g][i + t], -1e30f);
+                    p[t] = valid ? exp2_(y[i + t] - r + kShift) : 0.0f;
+                    l[i + t] = fmaf(p[t], inv_d, l[i + t]);
+                }
+                const uint32_t hi = e4m3x2(p[0], p[1]);
+                const float2 f = e4m3x2_f32(hi);
+                const uint32_t lo = e4m3x2((p[0] - f.x) * 16.0f, (p[1] - f.y) * 16.0f);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const uint32_t at = (uint32_t)((i + t) * 128) + (kc ^ (uint32_t)(((i + t) & 7) << 4));
+                    pb[at] = (uint8_t)(hi >> (8 * t));
+                    pb[at + N * 128] = (uint8_t)(lo >> (8 * t));
+                }
+            }
+            fence_async_smem();
+            mbar_arrive(bars.p_full(b));
+        }
+        if (give_up) break;
+        // the unit's sums and maxima over the group's 128 keys
+        float inv[16];
+        if (u.tiles > 0) {
+            const float ws = transpose_reduce<false>(l, lane), wm = transpose_reduce<true>(mx, lane);
+            if ((lane & 1) == 0) {
+                T->lsum[g][lane >> 1][q] = ws;
+                T->mx[g][lane >> 1][q] = wm;
+            }
+            ok = ok && wait_warp(bars.o_done(), (kt - 1) & 1u, abort_flag);
+            tc_fence_after();
+            named_bar(bar_id, 128);
+            ++nu;
+        }
+        const float *lrow = &T->lsum[g][0][0];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = 0.0f;
+            if (u.tiles > 0) {
+                const float4 s4 = *reinterpret_cast<const float4 *>(lrow + 4 * i);
+                s = (s4.x + s4.y) + (s4.z + s4.w);
+            }
+            l[i] = s;
+            inv[i] = s == 0.0f ? 0.0f : 1.0f / s;
+        }
+        if (q == 0 && lane < heads && row_ok) {
+            float s = 0.0f, m = -kInf, r = -kInf;
+            if (u.tiles > 0) {
+                const float4 s4 = *reinterpret_cast<const float4 *>(lrow + 4 * lane);
+                const float4 m4 = *reinterpret_cast<const float4 *>(T->mx[g][lane]);
+                s = (s4.x + s4.y) + (s4.z + s4.w);
+                m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+                r = T->ref[g][lane];
+            }
+            if (u.part >= 0) {
+                float *st = P.part_stat + ((int64_t)u.part * N + 16 * g + lane) * 3;
+                st[0] = r;
+                st[1] = s;
+                st[2] = m;
+            } else if (P.smax) {
+                P.smax[head_at + lane] = m > -kInf ? m * kLn2 : m;
+                P.ssum[head_at + lane] = m > -kInf ? s * exp2_(fmaxf(r, -1e30f) - kShift - m) : s;
+            }
+        }
+        for (int c = 0; c < P.blocks; ++c) {
+            float o[16];
+            if (u.tiles > 0) {
+                uint32_t hi[16], lo[16];
+                const uint32_t at = tmem + lanes + 2 * kSCols<N> + c * 2 * N + 16 * g;
+                tmem_ld16_nowait(at, hi);
+                tmem_ld16_nowait(at + N, lo);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[i] = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+            }
+            if (!row_ok) continue;
+            if (u.part >= 0) {
+                float *po = P.part_o + ((int64_t)u.part * N + 16 * g) * P.Dm + 128 * c + key;
+                if (u.tiles > 0)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (i < heads) po[(int64_t)i * P.Dm] = o[i];
+            } else {
+                uint16_t *po = P.out + head_at * P.Dm + 128 * c + key;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i < heads) po[(int64_t)i * P.Dm] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv[i]));
+            }
+        }
+        if (u.tiles > 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.o_empty());
+        }
+        named_bar(bar_id, 128);         // sums, maxima and references are read before they are reset
+    }
+    T->abort_flag = 1;
+}
+
+template <int N>
+__global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const __grid_constant__ Params P) {
+    using R = Roles<N>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0 && P.status) atomicOr(P.status, kDevErrInternal);
+        return;
+    }
+    Tail *T = reinterpret_cast<Tail *>(smem + kTailOff);
+    Bars bars{smem_u32(smem) + kTailOff};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bars.u_full(i), 1);
+            mbar_init(bars.u_empty(i), 2 + R::kSoft + R::kPrep + kGatherWarps);
+            mbar_init(bars.q_full(i), 32 * R::kPrep);
+            mbar_init(bars.q_empty(i), 1);
+            mbar_init(bars.s_full(i), 1);
+            mbar_init(bars.s_empty(i), R::kSoft);
+            mbar_init(bars.p_full(i), 32 * R::kSoft);
+            mbar_init(bars.p_empty(i), 1);
+        }
+        mbar_init(bars.o_done(), 1);
+        mbar_init(bars.o_empty(), R::kSoft);
+        for (int i = 0; i < kTileRing; ++i) {
+            mbar_init(bars.tile_full(i), 32 * kGatherWarps);
+            mbar_init(bars.meta_full(i), 32 * kGatherWarps);
+        }
+        for (int i = 0; i < kMaxSlots; ++i) mbar_init(bars.slot_empty(i), 1);
+        T->abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == R::kQk) {
+        tmem_alloc(smem_u32(&T->tmem), P.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = T->tmem;
+
+    if (warp < R::kSoft) {
+        softmax_role<N>(P, smem, T, bars, tmem);
+    } else if (warp < R::kGather0) {
+        prep_role<N>(P, smem, T, bars);
+    } else if (warp < R::kSched) {
+        gather_role<N>(P, smem, T, bars);
+    } else if (warp == R::kSched) {
+        scheduler_role(P, T, bars);
+    } else if (warp == R::kQk) {
+        if (lane == 0) qk_role<N>(P, smem, T, bars, tmem);
+        __syncwarp();
+    } else {
+        if (lane == 0) pv_role<N>(P, smem, T, bars, tmem);
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && T->abort_flag && P.status) atomicOr(P.status, LI_DEVERR_TIMEOUT);
+    if (warp == R::kQk) {
+        tc_fence_after();
+        tmem_dealloc(tmem, P.tmem_cols);
+    }
+}
+
+// Joins the partial outputs of units that were cut between CTAs: with references r_i, sums l_i and
+// outputs o_i of the pieces, o = sum o_i 2^(r_i - r) / sum l_i 2^(r_i - r), r = max r_i. A unit
+// that lies in one CTA's share was written by it.
+constexpr int kJoinThreads = 128;
+__global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __grid_constant__ Params P, int N, int grid) {
+    const int64_t unit = blockIdx.x;
+    const int64_t total = P.units * P.tiles;
+    auto cta_of = [&](int64_t t) { return (int)(((t + 1) * grid + total - 1) / total - 1); };
+    const int c0 = cta_of(unit * P.tiles), c1 = cta_of((unit + 1) * P.tiles - 1);
+    if (c0 == c1) return;
+    const int64_t row = unit / P.head_blocks;
+    const int head0 = (int)(unit - row * P.head_blocks) * 32;
+    const int h = blockIdx.y;
+    if (head0 + h >= P.G || !idx_ok(row, P.rows, P.status)) return;
+    const float kInf = __int_as_float(0x7f800000);
+    // the unit's pieces: the first starts it (slot 1 of its CTA), the others continue (slot 0)
+    float r = -kInf, m = -kInf;
+    for (int c = c0; c <= c1; ++c) {
+        const float *st = P.part_stat + ((int64_t)(2 * c + (c == c0)) * N + h) * 3;
+        r = fmaxf(r, st[0]);
+        m = fmaxf(m, st[2]);
+    }
+    const float rr = fmaxf(r, -1e30f);
+    float l = 0.0f;
+    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = c0; c <= c1; ++c) {
+        const int64_t slot = (int64_t)(2 * c + (c == c0)) * N + h;
+        const float *st = P.part_stat + slot * 3;
+        if (st[1] == 0.0f) continue;                    // no key of this piece counts
+        const float w = exp2_(fmaxf(st[0], -1e30f) - rr);
+        l = fmaf(st[1], w, l);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < P.blocks) o[i] = fmaf(P.part_o[slot * P.Dm + 128 * i + threadIdx.x], w, o[i]);
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t at = row * P.G + head0 + h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < P.blocks)
+            P.out[at * P.Dm + 128 * i + threadIdx.x] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv));
+    if (threadIdx.x == 0 && P.smax) {
+        P.smax[at] = m > -kInf ? m * kLn2 : m;
+        P.ssum[at] = m > -kInf ? l * exp2_(rr - kShift - m) : l;
+    }
+}
+
+}  // namespace
+
+bool cache_attn_plan(const li_cache_attn_args &a, CacheAttnPlan *p) {
+    const int sms = device_sm_count();
+    p->N = a.G <= 16 ? 16 : 32;
+    p->head_blocks = (a.G + 31) / 32;
+    p->tiles = (a.topk + kKeys - 1) / kKeys;
+    p->blocks = a.Dm / 128;
+    p->units = (int64_t)a.batch * a.s1 * p->head_blocks;
+    const int per_tile = p->blocks + (a.Dr > 0 ? 1 : 0);
+    p->q_bytes = (uint32_t)(p->blocks * 2 * p->N * 128 + (a.Dr > 0 ? p->N * 128 : 0));
+    const uint32_t p_bytes = 2u * 2u * p->N * 128u;
+    p->slots = 0;
+    // two q buffers where two whole tiles still fit, so that a unit's q is ready when it starts
+    for (int bufs = 2; bufs >= 1; --bufs) {
+        const uint32_t off = bufs * p->q_bytes;
+        const uint32_t slot_off = (off + p_bytes + 1023u) / 1024u * 1024u;
+        if (slot_off >= kTailOff) continue;
+        int slots = (int)((kTailOff - slot_off) / kSlot);
+        slots = slots < kMaxSlots ? slots : kMaxSlots;
+        // the gather runs at most this many tiles ahead of the softmax (the rings of kTileRing)
+        if (slots > (kTileRing - 2) * per_tile) slots = (kTileRing - 2) * per_tile;
+        if (slots < 2 * per_tile) continue;
+        p->q_bufs = bufs;
+        p->p_off = off;
+        p->slot_off = slot_off;
+        p->slots = slots;
+        break;
+    }
+    if (p->slots == 0) return false;
+    uint32_t cols = 32;
+    while (cols < (uint32_t)(8 * p->N + 2 * p->N * p->blocks)) cols <<= 1;
+    p->tmem_cols = cols;
+    const int64_t total = p->units * p->tiles;
+    p->split = p->units < 4 * (int64_t)sms && p->tiles > 1;
+    const int64_t most = p->split ? total : p->units;
+    p->grid = (int)(most < sms ? most : sms);
+    p->partial_floats = p->split ? (size_t)2 * p->grid * p->N * (a.Dm + 3) : 0;
+    return true;
+}
+
+cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnPlan &p, float *partial,
+                                   void *out, float *smax, float *ssum, cudaStream_t st) {
+    if (p.units == 0) return cudaSuccess;
+    Params P{};
+    P.q = static_cast<const uint16_t *>(a.q);
+    P.q_rope = static_cast<const uint16_t *>(a.q_rope);
+    P.codes = static_cast<const uint8_t *>(a.codes);
+    P.descale = a.descale;
+    P.k_rope = static_cast<const uint16_t *>(a.k_rope);
+    P.indices = a.sparse_indices;
+    P.status = a.device_status;
+    P.out = static_cast<uint16_t *>(out);
+    P.smax = smax;
+    P.ssum = ssum;
+    if (p.split) {
+        P.part_o = partial;
+        P.part_stat = partial + (size_t)2 * p.grid * p.N * a.Dm;
+    }
+    if (a.layout_k == LI_LAYOUT_PA_BSND) {
+        P.block_table = a.block_table;
+        P.bt_stride = a.block_table_stride;
+        P.block_size = a.block_size;
+        P.num_blocks = a.num_blocks;
+        P.key_rows = (int64_t)a.num_blocks * a.block_size;
+    } else {
+        P.key_rows = (int64_t)a.batch * a.s2;
+    }
+    P.units = p.units;
+    P.scale = a.scale;
+    P.rows = a.batch * a.s1;
+    P.s1 = a.s1;
+    P.s2 = a.s2;
+    P.G = a.G;
+    P.Dm = a.Dm;
+    P.topk = a.topk;
+    P.has_rope = a.Dr > 0;
+    P.blocks = p.blocks;
+    P.head_blocks = p.head_blocks;
+    P.tiles = p.tiles;
+    P.split = p.split;
+    P.q_bufs = p.q_bufs;
+    P.slots = p.slots;
+    P.q_bytes = p.q_bytes;
+    P.p_off = p.p_off;
+    P.slot_off = p.slot_off;
+    P.tmem_cols = p.tmem_cols;
+    auto run = [&](auto kern, int threads) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+        if (e != cudaSuccess) return e;
+        kern<<<p.grid, threads, kSmemBytes, st>>>(P);
+        return cudaGetLastError();
+    };
+    cudaError_t e = p.N == 16 ? run(cache_attn_kernel<16>, Roles<16>::kThreads)
+                              : run(cache_attn_kernel<32>, Roles<32>::kThreads);
+    if (e != cudaSuccess || !p.split) return e;
+    const dim3 grid((unsigned)p.units, (unsigned)(a.G < 32 ? a.G : 32));
+    cache_attn_join_kernel<<<grid, kJoinThreads, 0, st>>>(P, p.N, p.grid);
+    return cudaGetLastError();
+}
+
+}  // namespace li

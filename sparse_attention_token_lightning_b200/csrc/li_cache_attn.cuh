@@ -1,0 +1,29 @@
+// Attention over selected rows of the E4M3 key cache (li_cache_attn.cu): work split, shared-memory
+// plan and launcher.
+#pragma once
+
+#include "li_internal.cuh"
+
+namespace li {
+
+struct CacheAttnPlan {
+    int N;                      // heads per CTA, padded (16 or 32): MMA N is 2 N (hi and lo parts)
+    int head_blocks;            // CTAs' head ranges per row
+    int tiles;                  // 128-entry tiles of a row's selection
+    int64_t units;              // rows x head_blocks
+    int grid;
+    int split;                  // 1: each CTA takes an equal range of all units' tiles
+    int blocks;                 // 128-dim blocks of a key (Dm / 128)
+    int q_bufs, slots;
+    uint32_t q_bytes, p_off, slot_off;
+    uint32_t tmem_cols;
+    size_t partial_floats;      // split: partial outputs and statistics in the workspace
+};
+
+// False when the argument set does not fit the kernel.
+bool cache_attn_plan(const li_cache_attn_args &a, CacheAttnPlan *p);
+
+cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnPlan &p, float *partial,
+                                   void *out, float *smax, float *ssum, cudaStream_t st);
+
+}  // namespace li

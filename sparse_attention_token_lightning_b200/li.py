@@ -6,10 +6,12 @@ functions keep the C names (``li_metadata``, ``li_indexer``, ``li_merge_topk``, 
 workspaces with torch and call the library on the current stream; ``HostPipeline`` runs the
 indexer over host-resident problems with the copies overlapping the kernels. ``rope()`` /
 ``rope_grad()`` rotate queries and keys, ``cache_write()`` / ``cache_read()`` keep keys as E4M3
-codes with a scale per row. There is no fallback: if the library is missing, loading raises.
+codes with a scale per row and ``cache_attention()`` attends over selected rows of such a cache.
+There is no fallback: if the library is missing, loading raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from pathlib import Path
 
@@ -71,7 +73,8 @@ EXPORTS = ("li_metadata_workspace_size", "li_metadata", "li_indexer_workspace_si
            "li_abi_version", "li_indexer_noalloc", "li_plan", "li_merge_topk",
            "li_kl_grad_workspace_size", "li_kl_grad", "li_sparse_attention_workspace_size",
            "li_sparse_attention", "li_rope", "li_rope_grad", "li_rope_frequencies",
-           "li_cache_write", "li_cache_read")
+           "li_cache_write", "li_cache_read", "li_cache_attention_workspace_size",
+           "li_cache_attention")
 
 MERGE_MAX_LISTS = 16          # LI_MERGE_MAX_LISTS
 
@@ -160,6 +163,21 @@ class LiCacheArgs(ctypes.Structure):
     ]
 
 
+class LiCacheAttnArgs(ctypes.Structure):
+    """Mirror of li_cache_attn_args (include/li.h)."""
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("q_rope", ctypes.c_void_p), ("codes", ctypes.c_void_p),
+        ("descale", ctypes.c_void_p), ("k_rope", ctypes.c_void_p),
+        ("sparse_indices", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+        ("device_status", ctypes.c_void_p), ("block_table_stride", ctypes.c_int64),
+        ("scale", ctypes.c_float), ("batch", ctypes.c_int32), ("s1", ctypes.c_int32),
+        ("s2", ctypes.c_int32), ("G", ctypes.c_int32), ("Dm", ctypes.c_int32),
+        ("Dr", ctypes.c_int32), ("topk", ctypes.c_int32), ("layout_k", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 def lib_path() -> Path:
     return _LIB_PATH
 
@@ -215,7 +233,10 @@ def load(path) -> ctypes.CDLL:
                                       ctypes.POINTER(ctypes.c_float)]
     L.li_cache_write.argtypes = [ctypes.POINTER(LiCacheArgs), vp]
     L.li_cache_read.argtypes = [ctypes.POINTER(LiCacheArgs), vp]
-    for f in ("li_rope", "li_rope_grad", "li_rope_frequencies", "li_cache_write", "li_cache_read"):
+    L.li_cache_attention_workspace_size.argtypes = [ctypes.POINTER(LiCacheAttnArgs), sz]
+    L.li_cache_attention.argtypes = [ctypes.POINTER(LiCacheAttnArgs), vp, ctypes.c_size_t, vp, vp, vp, vp]
+    for f in ("li_rope", "li_rope_grad", "li_rope_frequencies", "li_cache_write", "li_cache_read",
+              "li_cache_attention_workspace_size", "li_cache_attention"):
         getattr(L, f).restype = ctypes.c_int
     L.li_abi_version.argtypes = []
     L.li_abi_version.restype = ctypes.c_int32
@@ -478,15 +499,27 @@ def sparse_attention(ap, stream=None, check: bool = True):
 
 # ---- rotary positions and the quantised key cache ------------------------------------------------
 
+_HERE = contextlib.nullcontext()
+
+
+def _using(dev):
+    """A context in which `dev` is the current device."""
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _raw_stream(dev, stream):
+    """Handle of `stream`, or of the device's current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index) or None
+    if stream.device != dev:
+        raise ValueError(f"a stream of {stream.device} with tensors on {dev}")
+    return stream.cuda_stream or None
+
+
 def _on_device(call, args, dev, stream):
     """call(args, stream) with `dev` current: on `stream`, or on the device's current stream."""
-    handle = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None
-              else stream.cuda_stream)
-    if dev.index == torch.cuda.current_device():
-        _check(call(ctypes.byref(args), handle or None))
-        return
-    with torch.cuda.device(dev):
-        _check(call(ctypes.byref(args), handle or None))
+    with _using(dev):
+        _check(call(ctypes.byref(args), _raw_stream(dev, stream)))
 
 
 def _empty(like, shape, dtype, stream):
@@ -730,6 +763,83 @@ def cache_read(codes, descale, out, rope_cache=None, rope_out=None, seqused_k=No
                         cu_seqlens, seqused, False, device_status)
     _checked(lib().li_cache_read, a, out.device, stream, device_status, check)
     return out, rope_out
+
+
+def make_cache_attn_args(q, codes, descale, sparse_indices, scale, q_rope=None, rope_cache=None,
+                         block_table=None, s2=None, device_status=None) -> LiCacheAttnArgs:
+    """li_cache_attn_args of device tensors (see cache_attention)."""
+    dev = q.device
+    if q.dim() != 4:
+        raise ValueError("q must be (B, S1, G, Dm)")
+    B, S1, G, Dm = q.shape
+    a = LiCacheAttnArgs()
+    a.q = _contiguous(q, dev, "q", torch.bfloat16)
+    codes = _no_head(codes, 3, "codes")
+    grid = codes.shape[:2]
+    a.codes = _contiguous(codes, dev, "codes", torch.float8_e4m3fn, (*grid, Dm))
+    a.descale = _contiguous(descale, dev, "descale", torch.float32, grid)
+    topk = sparse_indices.shape[-1]
+    a.sparse_indices = _contiguous(sparse_indices, dev, "sparse_indices", torch.int32, (B, S1, 1, topk))
+    a.scale, a.batch, a.s1, a.G, a.Dm, a.topk = float(scale), B, S1, G, Dm, topk
+    if (q_rope is None) != (rope_cache is None):
+        raise ValueError("q_rope and rope_cache go together")
+    if q_rope is not None:
+        R = q_rope.shape[-1]
+        a.q_rope = _contiguous(q_rope, dev, "q_rope", torch.bfloat16, (B, S1, G, R))
+        a.k_rope = _contiguous(_no_head(rope_cache, 3, "rope_cache"), dev, "rope_cache",
+                               torch.bfloat16, (*grid, R))
+        a.Dr = R
+    if block_table is not None:
+        if block_table.dim() != 2 or block_table.shape[0] != B:
+            raise ValueError(f"block_table must be ({B}, blocks), got {tuple(block_table.shape)}")
+        a.layout_k = LAYOUTS["PA_BSND"]
+        a.block_table = _contiguous(block_table, dev, "block_table", torch.int32)
+        a.block_table_stride = block_table.shape[1]
+        a.num_blocks, a.block_size = grid
+        a.s2 = block_table.shape[1] * grid[1] if s2 is None else s2
+    else:
+        if grid[0] != B or (s2 is not None and s2 != grid[1]):
+            raise ValueError(f"a dense cache of shape {tuple(grid)} with B={B}, s2={s2}")
+        a.s2 = grid[1]
+    if device_status is not None:
+        if device_status.element_size() != 4:
+            raise ValueError("device_status must be a 4-byte tensor")
+        a.device_status = _contiguous(device_status, dev, "device_status")
+    return a
+
+
+def cache_attention(q, codes, descale, sparse_indices, scale, q_rope=None, rope_cache=None,
+                    block_table=None, s2=None, return_stats: bool = False, device_status=None,
+                    stream=None, check: bool = True):
+    """Attention of q (B, S1, G, Dm), bf16, over selected rows of an E4M3 cache
+    (li_cache_attention): codes / descale / rope_cache as cache_write fills them, paged with
+    block_table (s2: the positions it may address, its whole width when None) or dense;
+    sparse_indices (B, S1, 1, topk) as li_indexer returns them without offsets. Returns out (B, S1,
+    G, Dm) bf16, or (out, softmax_max, softmax_sum) with return_stats, (B, 1, S1, G) fp32."""
+    a = make_cache_attn_args(q, codes, descale, sparse_indices, scale, q_rope, rope_cache,
+                             block_table, s2, device_status)
+    dev = q.device
+    L = lib()
+    n = ctypes.c_size_t(0)
+    own = check and device_status is None
+    if own:
+        device_status = _empty_status(dev, stream)
+        a.device_status = device_status.data_ptr()
+    with _using(dev):
+        _check(L.li_cache_attention_workspace_size(ctypes.byref(a), ctypes.byref(n)))
+        ws = _empty(q, n.value, torch.uint8, stream)
+        out = _empty(q, q.shape, torch.bfloat16, stream)
+        smax = ssum = None
+        if return_stats:
+            shape = (q.shape[0], 1, q.shape[1], q.shape[2])
+            smax, ssum = (_empty(q, shape, torch.float32, stream) for _ in range(2))
+        _check(L.li_cache_attention(ctypes.byref(a), ws.data_ptr(), n.value, out.data_ptr(), _ptr(smax),
+                                    _ptr(ssum), _raw_stream(dev, stream)))
+        if check:
+            st, bits = li_check_status(device_status, stream)
+            if st != LI_OK:
+                raise LiError(st, f"{li_last_error_string()} (device bits 0x{bits:x})")
+    return (out, smax, ssum) if return_stats else out
 
 
 class HostPipeline:

@@ -157,3 +157,59 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(L):
     assert li._row_stride(torch.zeros(1, 5, 2, 8)[:, ::2], 2, "x") == (3, 32)
     with pytest.raises(ValueError):
         li._row_stride(torch.zeros(4, 5, 2, 8)[:, :3], 2, "x")
+
+
+def test_cache_attention_mirror_matches_the_header(tmp_path):
+    test_mirrors_match_the_header(tmp_path, li.LiCacheAttnArgs, "li_cache_attn_args")
+
+
+def _cattn(**kw):
+    a = li.LiCacheAttnArgs()
+    a.q, a.codes, a.descale, a.sparse_indices = 0x10000, 0x20000, 0x30000, 0x40000
+    a.block_table, a.block_table_stride, a.num_blocks, a.block_size = 0x50000, 4, 9, 16
+    a.scale, a.batch, a.s1, a.s2, a.G, a.Dm, a.topk, a.layout_k = 0.05, 2, 3, 64, 16, 512, 32, 2
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+_DENSE_ATTN = dict(layout_k=0, block_table=None, block_table_stride=0, num_blocks=0, block_size=0)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(G=0), dict(G=129), dict(Dm=64), dict(Dm=200), dict(Dm=640), dict(Dr=32), dict(Dr=64),
+    dict(Dr=64, q_rope=0x60000), dict(q_rope=0x60000, k_rope=0x70000), dict(topk=0), dict(topk=8193),
+    dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
+    dict(batch=-1), dict(s1=-1), dict(s2=0), dict(s2=-1), dict(q=None), dict(codes=None),
+    dict(descale=None), dict(sparse_indices=None), dict(block_table=None), dict(layout_k=1),
+    dict(block_size=0), dict(block_size=1025), dict(num_blocks=0), dict(block_table_stride=3),
+    dict(_DENSE_ATTN, block_size=4), dict(_DENSE_ATTN, block_table=0x50000), dict(q=0x10008),
+    dict(codes=0x20008), dict(descale=0x30002), dict(sparse_indices=0x40001),
+    dict(device_status=0x60002), dict(reserved=1),
+    dict(Dr=64, q_rope=0x60008, k_rope=0x70000), dict(Dr=64, q_rope=0x60000, k_rope=0x70008)])
+def test_cache_attention_refusals(L, kw):
+    n = ctypes.c_size_t(0)
+    assert L.li_cache_attention_workspace_size(ctypes.byref(_cattn(**kw)), ctypes.byref(n)) == 1, kw
+    assert L.li_cache_attention(ctypes.byref(_cattn(**kw)), 0x100000, 1 << 40, 0x200000, None, None, None) == 1
+    assert li.li_last_error_string()
+
+
+def test_cache_attention_outputs_workspace_and_limits(L):
+    n = ctypes.c_size_t(0)
+    size = L.li_cache_attention_workspace_size
+    assert size(ctypes.byref(_cattn()), ctypes.byref(n)) == 0 and n.value % 256 == 0 and n.value > 0
+    need = n.value
+    run = lambda ws, b, out, m=None, s=None: L.li_cache_attention(ctypes.byref(_cattn()), ws, b, out, m, s, None)  # noqa: E731
+    assert run(None, need, 0x200000) == 3 and run(0x100010, need, 0x200000) == 3
+    assert run(0x100000, need - 256, 0x200000) == 3
+    assert run(0x100000, need, None) == 1 and run(0x100000, need, 0x200008) == 1
+    assert run(0x100000, need, 0x200000, 0x300000) == 1 and run(0x100000, need, 0x200000, 0x300000, 0x400002) == 1
+    assert size(ctypes.byref(_cattn(batch=1 << 14, s1=1 << 11)), ctypes.byref(n)) == 2
+    assert size(ctypes.byref(_cattn(num_blocks=1 << 25, block_size=128)), ctypes.byref(n)) == 2
+    # every head count and size of key fits; no rows need no launch
+    for G in (1, 16, 17, 32, 33, 128):
+        for Dm in (128, 256, 384, 512):
+            for rope in (dict(), dict(Dr=64, q_rope=0x60000, k_rope=0x70000)):
+                assert size(ctypes.byref(_cattn(G=G, Dm=Dm, **rope)), ctypes.byref(n)) == 0
+    empty = _cattn(batch=0)
+    assert L.li_cache_attention(ctypes.byref(empty), 0x100000, 1 << 30, None, None, None, None) == 0
