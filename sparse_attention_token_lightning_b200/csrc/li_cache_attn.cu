@@ -9,10 +9,10 @@
 //   q       times a power of two per head (largest element in [128, 256)) = hi + lo / 16, hi and
 //           lo in E4M3: 8 bits in 4 + 4, so every bf16 element down to 2^-13 of the row's largest
 //           is held exactly (and none is off by more than 2^-22 of it)
-//   weights with y = x log2(e) + log2(d_s), 2^(y - ref + 5) = hi + lo / 16 likewise (9 bits, half
-//           the error of a bf16 weight). The reference follows the largest y, not the largest x, so
-//           the scale is inside the exponent and the parts are full where the products are large;
-//           the normaliser sums 2^(y - ref + 5) / d_s in fp32.
+//   weights with y = x log2(e) + log2(d_s), 2^(y - ref) = hi + lo / 16 likewise (9 bits, half the
+//           error of a bf16 weight). The reference follows the largest y, not the largest x, so the
+//           scale is inside the exponent and the parts are full where the products are large; the
+//           normaliser sums 2^(y - ref) / d_s in fp32.
 // The products S = K Q^T (keys on M = 128, hi and lo heads on N) and O^T += V^T P^T (dims on M = 128,
 // the key tile read MN-major, keys on K) both read the same gathered tile; the rope part is a bf16
 // product of its own into other TMEM columns, since its codes have no scale.
@@ -20,9 +20,10 @@
 // One CTA per SM works on units (row, block of up to 32 heads), whole units in turn when there are
 // many rows, or an equal share of all units' tiles of 128 selected keys when there are few
 // (decode): a unit cut between CTAs leaves partial outputs, which a second kernel joins. Warps:
-//   softmax   4 per 16 heads: a thread owns one key of the tile and 16 heads. The reference moves
-//             only when some y exceeds it by more than 3 (every weight <= 2^8 of the 448 that E4M3
-//             holds); a vote per tile finds that out, the maxima are reduced only then
+//   softmax   two groups of 4 warps, each with half the heads: a thread owns one key of the tile and
+//             8 or 16 heads. The largest weight is set to 2^4 and may grow to 2^8 (E4M3 holds 448)
+//             before the reference moves; a vote per tile finds that out, and only then are the
+//             maxima reduced and O rescaled. Weights below 2^-18 of the largest may round to 0
 //   prep      the next unit's q: normalised, split and stored in the MMA layout
 //   gather    looks up each selected key's cache row, keeps its scale for the softmax warps and
 //             copies codes and rope part with cp.async into 16 KB slots (128 keys x 128 bytes,
@@ -51,17 +52,19 @@ constexpr uint32_t kSmemBytes = 232448;
 constexpr uint32_t kTailBytes = 8192;
 constexpr uint32_t kTailOff = kSmemBytes - kTailBytes;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 3.0f;                      // log2 units above the reference
-constexpr float kShift = 5.0f;                      // weights are 2^(y - ref + kShift) <= 2^8
+// A tile's largest weight is set to 2^kShift when the reference moves, and it moves when a weight
+// would pass 2^kTop (of the 448 that E4M3 holds).
+constexpr float kShift = 4.0f, kTop = 8.0f;
+constexpr float kNoRef = -1e30f;                    // reference of a piece without keys
 constexpr float kMinDescale = 7.888609052210118e-31f, kMaxDescale = 1.2676506002282294e30f;  // 2^+-100
 constexpr uint32_t kDevErrInternal = 0x20u;
 
 template <int N> struct Roles {
-    static constexpr int kGroups = N / 16;              // softmax groups of 4 warps, 16 heads each
-    static constexpr int kSoft = 4 * kGroups;
-    static constexpr int kPrep0 = kSoft, kPrep = N == 16 ? 4 : 2;
+    static constexpr int kHeads = N / 2;                // heads of a softmax thread
+    static constexpr int kSoft = 8;                     // two groups of 4 warps
+    static constexpr int kPrep0 = kSoft, kPrep = 4;
     static constexpr int kGather0 = kPrep0 + kPrep;
-    static constexpr int kSched = kGather0 + kGatherWarps, kQk = kSched + 1, kPv = kSched + 2;
+    static constexpr int kSched = kGather0 + kGatherWarps, kQk = kSched + 1;    // then pv
     static constexpr int kThreads = 32 * (kSched + 3);
 };
 
@@ -98,8 +101,9 @@ struct Tail {
     volatile int abort_flag;
     alignas(16) int vote[2][2][4];              // [group][tile parity][warp]
     alignas(16) float ah[kAhRing][32];          // scale log2(e) / the head's power of two
-    alignas(16) float ref[2][16];               // [group][head]
-    alignas(16) float alpha[2][16];
+    alignas(16) float ref[2][16];               // [group][head]: y of a weight 1
+    alignas(16) float alpha[2][16], moved[2][16];
+    int seen[2][16], fresh[2];                  // whether a head's reference is set; any that is not
     alignas(16) float red[2][16][4];            // [group][head][warp]
     alignas(16) float lsum[2][16][4], mx[2][16][4];
     alignas(16) float descale[kTileRing][kKeys];    // 0: the entry selects nothing
@@ -156,10 +160,53 @@ __device__ __forceinline__ float exp2_(float x) {
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
+__device__ __forceinline__ uint32_t e4m3x2(__half2 v) {
+    return __nv_cvt_halfraw2_to_fp8x2((__half2_raw)v, __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ __half2 e4m3x2_h2(uint32_t v) {
+    return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3));
+}
 __device__ __forceinline__ float2 e4m3x2_f32(uint32_t v) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3);
     return __half22float2(__half2(h));
 }
+// n consecutive fp32 columns of this thread's TMEM lane, without the wait.
+__device__ __forceinline__ void tmem_ld_nowait(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16_nowait(taddr, r); }
+__device__ __forceinline__ void tmem_ld_nowait(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_nowait(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_nowait(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The weights operand: row = key, 2 N bytes (hi of N heads, then lo), i.e. an MN-major B whose rows
+// are one swizzle span: 32 bytes (N = 16) or 64 (N = 32); eight keys form an atom.
+template <int N> __device__ __forceinline__ uint64_t weights_desc(uint32_t saddr) {
+    constexpr uint64_t kType = N == 16 ? 6 : 4;         // 32- or 64-byte swizzle
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)((16 * N) >> 4) << 32) |
+           ((uint64_t)1 << 46) | (kType << 61);
+}
+// Byte of chunk c (16 heads) in row `key`.
+template <int N> __device__ __forceinline__ uint32_t weights_at(int key, int c) {
+    const int x = N == 16 ? (key >> 2) & 1 : (key >> 1) & 3;
+    return (uint32_t)(key * 2 * N + ((c ^ x) << 4));
+}
+
 // Largest of v over the warp (NaN counts as -infinity).
 __device__ __forceinline__ float warp_max(float v) {
     int i = __float_as_int(v == v ? v : -__int_as_float(0x7f800000));
@@ -167,28 +214,29 @@ __device__ __forceinline__ float warp_max(float v) {
     i = __reduce_max_sync(0xffffffffu, i);
     return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
 }
-// Sums (or maxima) of 16 values over the warp: lane l returns value 8 (l >> 4) + 4 (l >> 3 & 1) +
-// 2 (l >> 2 & 1) + (l >> 1 & 1), i.e. value l >> 1.
-template <bool kMax>
-__device__ __forceinline__ float transpose_reduce(const float (&v)[16], int lane) {
-    float a[16];
+// Sums (or maxima) of H values over the warp, transposed: lane l returns value l / (32 / H).
+template <bool kMax, int H>
+__device__ __forceinline__ float transpose_reduce(const float (&v)[H], int lane) {
+    float a[H];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) a[i] = v[i];
+    for (int i = 0; i < H; ++i) a[i] = v[i];
+    int bit = 16;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        const int bit = 16 >> s, half = 8 >> s;
+    for (int half = H / 2; half >= 1; half >>= 1, bit >>= 1) {
         const bool up = (lane & bit) != 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < half) {
-                const float keep = up ? a[i + half] : a[i];
-                const float send = up ? a[i] : a[i + half];
-                const float recv = __shfl_xor_sync(0xffffffffu, send, bit);
-                a[i] = kMax ? fmaxf(keep, recv) : keep + recv;
-            }
+        for (int i = 0; i < half; ++i) {
+            const float keep = up ? a[i + half] : a[i];
+            const float send = up ? a[i] : a[i + half];
+            const float recv = __shfl_xor_sync(0xffffffffu, send, bit);
+            a[i] = kMax ? fmaxf(keep, recv) : keep + recv;
+        }
     }
-    const float o = __shfl_xor_sync(0xffffffffu, a[0], 1);
-    return kMax ? fmaxf(a[0], o) : a[0] + o;
+    for (; bit >= 1; bit >>= 1) {
+        const float o = __shfl_xor_sync(0xffffffffu, a[0], bit);
+        a[0] = kMax ? fmaxf(a[0], o) : a[0] + o;
+    }
+    return a[0];
 }
 
 // First tile of CTA c's share of all units' tiles.
@@ -333,37 +381,27 @@ __device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &b
 }
 
 // ---- gather ----------------------------------------------------------------------------------------
-// Cache row and scale of entry pos of the unit's row (-1, 0 where it selects nothing).
-__device__ __forceinline__ void look_up(const Params &P, const int32_t *ir, int64_t b, int pos, int32_t *row,
-                                        float *d, uint32_t *err) {
-    *row = -1;
-    *d = 0.0f;
-    const int32_t v = pos < P.topk ? __ldg(ir + pos) : -1;
-    if (v < 0) return;
+// The three dependent reads behind a selected key, one function each so that the loop can issue
+// them a tile apart: its position, the block that holds it, its cache row's scale.
+__device__ __forceinline__ int32_t entry_at(const Params &P, const int32_t *ir, int pos, int end) {
+    return pos < end ? __ldg(ir + pos) : -1;
+}
+__device__ __forceinline__ int32_t block_of(const Params &P, int64_t b, int32_t v) {
+    return P.block_table && v >= 0 && v < P.s2 ? __ldg(P.block_table + b * P.bt_stride + v / P.block_size) : 0;
+}
+// Cache row of position v, -1 where it selects nothing.
+__device__ __forceinline__ int32_t row_of(const Params &P, int64_t b, int32_t v, int32_t blk, uint32_t *err) {
+    if (v < 0) return -1;
     if (v >= P.s2) {
         *err |= LI_DEVERR_LENGTHS;
-        return;
+        return -1;
     }
-    int64_t r;
-    if (P.block_table) {
-        const int32_t q = v / P.block_size;
-        const int32_t blk = __ldg(P.block_table + b * P.bt_stride + q);
-        if (blk < 0 || blk >= P.num_blocks) {
-            *err |= LI_DEVERR_TABLE;
-            return;
-        }
-        r = (int64_t)blk * P.block_size + (v - q * P.block_size);
-    } else {
-        r = b * P.s2 + v;
+    if (!P.block_table) return (int32_t)(b * P.s2 + v);
+    if (blk < 0 || blk >= P.num_blocks) {
+        *err |= LI_DEVERR_TABLE;
+        return -1;
     }
-    if (!idx_ok(r, P.key_rows, P.status)) return;
-    const float s = __ldg(P.descale + r);
-    if (!(s >= kMinDescale && s <= kMaxDescale)) {
-        *err |= LI_DEVERR_DESCALE;
-        return;
-    }
-    *row = (int32_t)r;
-    *d = s;
+    return blk * P.block_size + v % P.block_size;
 }
 
 template <int N>
@@ -382,15 +420,18 @@ __device__ void gather_role(const Params &P, uint8_t *smem, Tail *T, const Bars 
         Unit u;
         if (!take_unit(T, bars, it, &u)) { ok = false; break; }
         if (u.row < 0) break;
+        if (u.tiles == 0) continue;
         const int32_t *ir = P.indices + (int64_t)u.row * P.topk;
         const int64_t b = u.row / P.s1;
-        int32_t mine = -1;
-        float d = 0.0f;
         int pos = u.tile0 * kKeys + 32 * w + lane;
-        if (u.tiles > 0) look_up(P, ir, b, pos, &mine, &d, &err);
-        for (int j = 0; j < u.tiles && ok; ++j, tr.next(kTileRing)) {
-            T->descale[tr.idx][32 * w + lane] = d;
-            mbar_arrive(bars.meta_full(tr.idx));
+        const int end = min((u.tile0 + u.tiles) * kKeys, P.topk);
+        int32_t v0 = entry_at(P, ir, pos, end), v1 = entry_at(P, ir, pos + kKeys, end);
+        int32_t v2 = entry_at(P, ir, pos + 2 * kKeys, end);
+        int32_t blk = block_of(P, b, v0), blk1 = block_of(P, b, v1);
+        int32_t mine = row_of(P, b, v0, blk, &err);
+        if (mine >= 0 && !idx_ok(mine, P.key_rows, P.status)) mine = -1;
+        float d = mine >= 0 ? __ldg(P.descale + mine) : 0.0f;
+        for (int j = 0; j < u.tiles; ++j, tr.next(kTileRing)) {
             int32_t row[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) row[i] = __shfl_sync(0xffffffffu, mine, sub + 4 * i);
@@ -417,8 +458,20 @@ __device__ void gather_role(const Params &P, uint8_t *smem, Tail *T, const Bars 
             }
             if (!ok) break;
             cp_async_arrive(bars.tile_full(tr.idx));
+            // a scale outside the range counts as no key: its codes meet weight 0
+            if (mine >= 0 && !(d >= kMinDescale && d <= kMaxDescale)) {
+                err |= LI_DEVERR_DESCALE;
+                d = 0.0f;
+            }
+            T->descale[tr.idx][32 * w + lane] = d;
+            mbar_arrive(bars.meta_full(tr.idx));
             pos += kKeys;
-            if (j + 1 < u.tiles) look_up(P, ir, b, pos, &mine, &d, &err);
+            mine = row_of(P, b, v1, blk1, &err);
+            if (mine >= 0 && !idx_ok(mine, P.key_rows, P.status)) mine = -1;
+            d = mine >= 0 ? __ldg(P.descale + mine) : 0.0f;
+            blk1 = block_of(P, b, v2);
+            v1 = v2;
+            v2 = entry_at(P, ir, pos + 2 * kKeys, end);
         }
     }
     // no copy may still be writing shared memory when the CTA leaves
@@ -482,7 +535,7 @@ __device__ void qk_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
 template <int N>
 __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bars, uint32_t tmem) {
     const uint32_t sbase = smem_u32(smem), slots = sbase + P.slot_off;
-    constexpr uint32_t idesc = (1u << 4) | (1u << 15) | ((2u * N >> 3) << 17) | (8u << 24);
+    constexpr uint32_t idesc = (1u << 4) | (1u << 15) | (1u << 16) | ((2u * N >> 3) << 17) | (8u << 24);
     Ring sr;
     uint32_t kt = 0, nu = 0;
     for (int it = 0;; ++it) {
@@ -498,14 +551,14 @@ __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
             if (!ok) break;
             fence_async_smem();
             tc_fence_after();
-            const uint64_t p = sw128_desc(sbase + P.p_off + (kt & 1u) * (2 * N * 128));
+            const uint64_t p = weights_desc<N>(sbase + P.p_off + (kt & 1u) * (2 * N * 128));
             if (P.has_rope) sr.next(P.slots);
             for (int c = 0; c < P.blocks; ++c, sr.next(P.slots)) {
                 const uint32_t va = slots + sr.idx * kSlot;
                 const uint32_t d = tmem + 2 * kSCols<N> + c * 2 * N;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    umma_f8(d, sw128_desc_mn(va + k * 32 * 128, kSlot), p + 2 * k, idesc, (j | k) != 0);
+                    umma_f8(d, sw128_desc_mn(va + k * 32 * 128, kSlot), p + k * (32 * 2 * N >> 4), idesc, (j | k) != 0);
                 umma_commit(bars.slot_empty(sr.idx));
             }
             umma_commit(bars.p_empty(kt & 1u));
@@ -518,223 +571,262 @@ __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
 }
 
 // ---- softmax and output ------------------------------------------------------------------------------
-template <int N>
+// Four consecutive floats of shared memory.
+__device__ __forceinline__ void lds4(const float *p, float (&v)[4]) {
+    const float4 t = *reinterpret_cast<const float4 *>(p);
+    v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+}
+
+template <int N, bool kStats>
 __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bars, uint32_t tmem) {
+    constexpr int H = Roles<N>::kHeads;                 // heads of a thread
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = warp >> 2, q = warp & 3;              // group (16 heads), quarter of the TMEM lanes
+    const int g = warp >> 2, q = warp & 3;              // group (H heads), quarter of the TMEM lanes
     const int key = 32 * q + lane;                      // key of the tile; dim of an O block
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const float kInf = __int_as_float(0x7f800000);
     volatile int *abort_flag = &T->abort_flag;
     const int bar_id = 1 + g;
+    const float rs = P.scale * kLog2e;
     Ring tr;
     uint32_t kt = 0;
     int nu = 0;
     bool ok = true;
     for (int it = 0;; ++it) {
-        Unit u;
         // the group's warps agree on giving up here too (a vote below carries a failure on)
         bool got = mbar_wait(bars.u_full(it & 1), (it >> 1) & 1, abort_flag);
         got = __all_sync(0xffffffffu, got) && ok;
         if (lane == 0) T->vote[g][kt & 1][q] = got ? 0 : 2;
+        if (q == 0 && lane < H) {
+            T->ref[g][lane] = 0.0f;
+            T->seen[g][lane] = 0;
+        }
         named_bar(bar_id, 128);
         {
             const int4 v = *reinterpret_cast<const int4 *>(T->vote[g][kt & 1]);
             if ((v.x | v.y | v.z | v.w) & 2) break;
         }
-        u = T->unit[it & 1];
+        const Unit u = T->unit[it & 1];
         named_bar(bar_id, 128);                         // the vote slot is written again below
         if (lane == 0) mbar_arrive(bars.u_empty(it & 1));
         if (u.row < 0) return;
-        const int heads = min(P.G - u.head0 - 16 * g, 16);      // may be <= 0
-        const int64_t head_at = (int64_t)u.row * P.G + u.head0 + 16 * g;
+        const int heads = min(P.G - u.head0 - H * g, H);        // may be <= 0
+        const int64_t head_at = (int64_t)u.row * P.G + u.head0 + H * g;
         const bool row_ok = idx_ok(u.row, P.rows, P.status);
-        float l[16], mx[16];
+        float l[H], mx[H];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) { l[i] = 0.0f; mx[i] = -kInf; }
-        if (u.tiles > 0 && q == 0 && lane < 16) T->ref[g][lane] = -kInf;
-        if (u.tiles > 0) named_bar(bar_id, 128);
-        bool give_up = false;
+        for (int i = 0; i < H; ++i) {
+            l[i] = 0.0f;
+            if (kStats) mx[i] = -kInf;
+        }
+        bool give_up = false, fresh = true;             // fresh: a head has no reference yet
+        const float *ah = T->ah[nu & (kAhRing - 1)] + H * g;
+        const float *ref = T->ref[g];
         for (int j = 0; j < u.tiles; ++j, ++kt, tr.next(kTileRing)) {
             const uint32_t b = kt & 1u;
             ok = ok && wait_warp(bars.meta_full(tr.idx), tr.phase, abort_flag);
+            // an entry that selects nothing has scale 0 and a weight of 2^-inf
             const float d = ok ? T->descale[tr.idx][key] : 0.0f;
-            const bool valid = d > 0.0f;
-            const float log2d = valid ? log2f(d) : 0.0f, inv_d = valid ? __frcp_rn(d) : 0.0f;
+            const float log2d = log2f(d), inv_d = d > 0.0f ? __frcp_rn(d) : 0.0f;
             ok = ok && wait_warp(bars.s_full(b), (kt >> 1) & 1u, abort_flag);
-            float y[16];
+            float t[H];                                 // y - ref, the weights' exponents
             tc_fence_after();
             {
-                uint32_t hi[16], lo[16];
-                const uint32_t s = tmem + lanes + b * kSCols<N> + 16 * g;
-                tmem_ld16_nowait(s, hi);
-                tmem_ld16_nowait(s + N, lo);
+                uint32_t hi[H], lo[H], rp[H];
+                const uint32_t s = tmem + lanes + b * kSCols<N> + H * g;
+                tmem_ld_nowait(s, hi);
+                tmem_ld_nowait(s + N, lo);
+                if (P.has_rope) tmem_ld_nowait(s + 2 * N, rp);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    y[i] = d * fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
-                const float *ah = T->ah[nu & (kAhRing - 1)] + 16 * g;
-                if (P.has_rope) {
-                    tmem_ld16_nowait(s + 2 * N, hi);
-                    tmem_wait_ld();
-                    const float rs = P.scale * kLog2e;
+                for (int i = 0; i < H; i += 4) {
+                    float a4[4];
+                    lds4(ah + i, a4);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) y[i] = fmaf(y[i], ah[i], rs * __uint_as_float(hi[i]));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) y[i] *= ah[i];
+                    for (int k = 0; k < 4; ++k) {
+                        const float sc = fmaf(__uint_as_float(lo[i + k]), 0.0625f, __uint_as_float(hi[i + k]));
+                        t[i + k] = fmaf(sc, d * a4[k], P.has_rope ? rs * __uint_as_float(rp[i + k]) : 0.0f);
+                    }
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.s_empty(b));
-            bool over = false;
+            float top = -kInf;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (valid) mx[i] = fmaxf(mx[i], y[i]);
-                y[i] = valid ? y[i] + log2d : -kInf;
-                over |= y[i] > T->ref[g][i] + kSlack;
+            for (int i = 0; i < H; i += 4) {
+                float r4[4];
+                lds4(ref + i, r4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (kStats && d > 0.0f) mx[i + k] = fmaxf(mx[i + k], t[i + k]);
+                    t[i + k] = (t[i + k] + log2d) - r4[k];
+                    top = fmaxf(top, t[i + k]);
+                }
             }
-            const bool any = __any_sync(0xffffffffu, over);
+            const bool any = __any_sync(0xffffffffu, top > kTop || (fresh && d > 0.0f));
             if (lane == 0) T->vote[g][b][q] = (any ? 1 : 0) | (ok ? 0 : 2);
             named_bar(bar_id, 128);
             const int4 v4 = *reinterpret_cast<const int4 *>(T->vote[g][b]);
             const int v = v4.x | v4.y | v4.z | v4.w;
             if (v & 2) { give_up = true; break; }
             if (v & 1) {
-                // the references move to the tile's maxima; O and the sums follow
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float m = warp_max(y[i]);
-                    if (lane == 0) T->red[g][i][q] = m;
+                // references with a larger weight than 2^kShift move to it, and a head's first one
+                // to its largest weight whatever it is; O and the sums follow
+                const float m = transpose_reduce<true>(t, lane);
+                if ((lane & (32 / H - 1)) == 0) T->red[g][lane / (32 / H)][q] = m;
+                named_bar(bar_id, 128);
+                if (q == 0 && lane < H) {
+                    float m4[4];
+                    lds4(T->red[g][lane], m4);
+                    const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    const bool seen = T->seen[g][lane] != 0;
+                    float up = seen ? fmaxf(most - kShift, 0.0f) : most > -kInf ? most - kShift : 0.0f;
+                    T->ref[g][lane] += up;
+                    T->alpha[g][lane] = seen ? exp2_(-up) : 0.0f;   // nothing is summed before the first
+                    T->moved[g][lane] = up;
+                    T->seen[g][lane] = seen || most > -kInf;
+                    const uint32_t mask = (1u << H) - 1u;
+                    const bool all = __all_sync(mask, seen || most > -kInf);
+                    if (lane == 0) T->fresh[g] = !all;
                 }
                 named_bar(bar_id, 128);
-                if (q == 0 && lane < 16) {
-                    const float4 m4 = *reinterpret_cast<const float4 *>(T->red[g][lane]);
-                    const float old = T->ref[g][lane];
-                    const float m = fmaxf(fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w)), old);
-                    T->ref[g][lane] = m;
-                    T->alpha[g][lane] = old > -kInf ? exp2_(old - m) : (m > -kInf ? 0.0f : 1.0f);
-                }
-                named_bar(bar_id, 128);
-                float al[16];
+                fresh = T->fresh[g] != 0;
+                uint32_t al[H];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    al[i] = T->alpha[g][i];
-                    l[i] *= al[i];
+                for (int i = 0; i < H; i += 4) {
+                    float a4[4], u4[4];
+                    lds4(T->alpha[g] + i, a4);
+                    lds4(T->moved[g] + i, u4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        al[i + k] = __float_as_uint(a4[k]);
+                        l[i + k] *= a4[k];
+                        t[i + k] -= u4[k];
+                    }
                 }
                 if (j > 0) {
                     ok = ok && wait_warp(bars.o_done(), (kt - 1) & 1u, abort_flag);
                     tc_fence_after();
-                    for (int c = 0; c < 2 * P.blocks; ++c) {
-                        const uint32_t o = tmem + lanes + 2 * kSCols<N> + c * N + 16 * g;
-                        float t[16];
-                        tmem_ld16(o, t);
+                    for (int c = 0; c < P.blocks; ++c) {
+                        const uint32_t o = tmem + lanes + 2 * kSCols<N> + c * 2 * N + H * g;
+                        uint32_t hi[H], lo[H];
+                        tmem_ld_nowait(o, hi);
+                        tmem_ld_nowait(o + N, lo);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) t[i] *= al[i];
-                        tmem_st16(o, t);
+                        for (int i = 0; i < H; ++i) {
+                            hi[i] = __float_as_uint(__uint_as_float(hi[i]) * __uint_as_float(al[i]));
+                            lo[i] = __float_as_uint(__uint_as_float(lo[i]) * __uint_as_float(al[i]));
+                        }
+                        tmem_st_nowait(o, hi);
+                        tmem_st_nowait(o + N, lo);
                     }
+                    tmem_wait_st();
                     tc_fence_before();
                 }
             }
             ok = ok && wait_warp(bars.p_empty(b), ((kt >> 1) & 1u) ^ 1u, abort_flag);
-            // weights as hi + lo / 16; rows of the MMA operand: head (hi), N + head (lo)
-            uint8_t *pb = smem + P.p_off + b * (2 * N * 128) + 16 * g * 128 + (key & 15);
-            const uint32_t kc = (uint32_t)(key >> 4) << 4;
+            // weights as hi + lo / 16, by way of fp16 (11 bits); a key's row of the operand
+            uint32_t hi[H / 4], lo[H / 4];
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                float p[2];
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    // a reference of -infinity is met only by y = -infinity: weight 0
-                    const float r = fmaxf(T->ref[g][i + t], -1e30f);
-                    p[t] = valid ? exp2_(y[i + t] - r + kShift) : 0.0f;
-                    l[i + t] = fmaf(p[t], inv_d, l[i + t]);
+            for (int i = 0; i < H; i += 2) {
+                const float p0 = exp2_(t[i]), p1 = exp2_(t[i + 1]);
+                l[i] = fmaf(p0, inv_d, l[i]);
+                l[i + 1] = fmaf(p1, inv_d, l[i + 1]);
+                const __half2 p = __floats2half2_rn(p0, p1);
+                const uint32_t h8 = e4m3x2(p);
+                const __half2 rem = __hfma2(e4m3x2_h2(h8), __float2half2_rn(-16.0f), __hmul2(p, __float2half2_rn(16.0f)));
+                const uint32_t l8 = e4m3x2(rem);
+                if (i & 2) {
+                    hi[i / 4] |= h8 << 16;
+                    lo[i / 4] |= l8 << 16;
+                } else {
+                    hi[i / 4] = h8;
+                    lo[i / 4] = l8;
                 }
-                const uint32_t hi = e4m3x2(p[0], p[1]);
-                const float2 f = e4m3x2_f32(hi);
-                const uint32_t lo = e4m3x2((p[0] - f.x) * 16.0f, (p[1] - f.y) * 16.0f);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const uint32_t at = (uint32_t)((i + t) * 128) + (kc ^ (uint32_t)(((i + t) & 7) << 4));
-                    pb[at] = (uint8_t)(hi >> (8 * t));
-                    pb[at + N * 128] = (uint8_t)(lo >> (8 * t));
-                }
+            }
+            uint8_t *pb = smem + P.p_off + b * (2 * N * 128);
+            if constexpr (H == 8) {
+                *reinterpret_cast<uint2 *>(pb + weights_at<N>(key, 0) + 8 * g) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2 *>(pb + weights_at<N>(key, 1) + 8 * g) = make_uint2(lo[0], lo[1]);
+            } else {
+                *reinterpret_cast<uint4 *>(pb + weights_at<N>(key, g)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(pb + weights_at<N>(key, 2 + g)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
             fence_async_smem();
             mbar_arrive(bars.p_full(b));
         }
         if (give_up) break;
         // the unit's sums and maxima over the group's 128 keys
-        float inv[16];
         if (u.tiles > 0) {
-            const float ws = transpose_reduce<false>(l, lane), wm = transpose_reduce<true>(mx, lane);
-            if ((lane & 1) == 0) {
-                T->lsum[g][lane >> 1][q] = ws;
-                T->mx[g][lane >> 1][q] = wm;
+            const float ws = transpose_reduce<false>(l, lane);
+            float wm = 0.0f;
+            if constexpr (kStats) wm = transpose_reduce<true>(mx, lane);
+            if ((lane & (32 / H - 1)) == 0) {
+                T->lsum[g][lane / (32 / H)][q] = ws;
+                if (kStats) T->mx[g][lane / (32 / H)][q] = wm;
             }
             ok = ok && wait_warp(bars.o_done(), (kt - 1) & 1u, abort_flag);
             tc_fence_after();
             named_bar(bar_id, 128);
             ++nu;
         }
-        const float *lrow = &T->lsum[g][0][0];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float s = 0.0f;
-            if (u.tiles > 0) {
-                const float4 s4 = *reinterpret_cast<const float4 *>(lrow + 4 * i);
-                s = (s4.x + s4.y) + (s4.z + s4.w);
-            }
-            l[i] = s;
-            inv[i] = s == 0.0f ? 0.0f : 1.0f / s;
+        for (int i = 0; i < H; ++i) {
+            float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (u.tiles > 0) lds4(T->lsum[g][i], s4);
+            const float s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+            l[i] = u.part >= 0 ? 1.0f : s == 0.0f ? 0.0f : 1.0f / s;
         }
-        if (q == 0 && lane < heads && row_ok) {
-            float s = 0.0f, m = -kInf, r = -kInf;
+        if (q == 0 && lane < heads && row_ok && (u.part >= 0 || kStats)) {
+            float s = 0.0f, m = -kInf, r = kNoRef;
             if (u.tiles > 0) {
-                const float4 s4 = *reinterpret_cast<const float4 *>(lrow + 4 * lane);
-                const float4 m4 = *reinterpret_cast<const float4 *>(T->mx[g][lane]);
-                s = (s4.x + s4.y) + (s4.z + s4.w);
-                m = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
-                r = T->ref[g][lane];
+                float s4[4], m4[4];
+                lds4(T->lsum[g][lane], s4);
+                s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                if constexpr (kStats) {
+                    lds4(T->mx[g][lane], m4);
+                    m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                }
+                if (T->seen[g][lane]) r = ref[lane];
             }
             if (u.part >= 0) {
-                float *st = P.part_stat + ((int64_t)u.part * N + 16 * g + lane) * 3;
+                float *st = P.part_stat + ((int64_t)u.part * N + H * g + lane) * 3;
                 st[0] = r;
                 st[1] = s;
                 st[2] = m;
-            } else if (P.smax) {
+            } else {
                 P.smax[head_at + lane] = m > -kInf ? m * kLn2 : m;
-                P.ssum[head_at + lane] = m > -kInf ? s * exp2_(fmaxf(r, -1e30f) - kShift - m) : s;
+                P.ssum[head_at + lane] = m > -kInf ? s * exp2_(r - m) : s;
             }
         }
         for (int c = 0; c < P.blocks; ++c) {
-            float o[16];
+            float o[H];
+#pragma unroll
+            for (int i = 0; i < H; ++i) o[i] = 0.0f;
             if (u.tiles > 0) {
-                uint32_t hi[16], lo[16];
-                const uint32_t at = tmem + lanes + 2 * kSCols<N> + c * 2 * N + 16 * g;
-                tmem_ld16_nowait(at, hi);
-                tmem_ld16_nowait(at + N, lo);
+                uint32_t hi[H], lo[H];
+                const uint32_t at = tmem + lanes + 2 * kSCols<N> + c * 2 * N + H * g;
+                tmem_ld_nowait(at, hi);
+                tmem_ld_nowait(at + N, lo);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    o[i] = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+                for (int i = 0; i < H; ++i)
+                    o[i] = l[i] * fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
             }
             if (!row_ok) continue;
             if (u.part >= 0) {
-                float *po = P.part_o + ((int64_t)u.part * N + 16 * g) * P.Dm + 128 * c + key;
-                if (u.tiles > 0)
+                if (u.tiles == 0) continue;             // its sum of 0 says that nothing is there
+                float *po = P.part_o + ((int64_t)u.part * N + H * g) * P.Dm + 128 * c + key;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (i < heads) po[(int64_t)i * P.Dm] = o[i];
+                for (int i = 0; i < H; ++i)
+                    if (i < heads) po[(int64_t)i * P.Dm] = o[i];
             } else {
                 uint16_t *po = P.out + head_at * P.Dm + 128 * c + key;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (i < heads) po[(int64_t)i * P.Dm] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv[i]));
+                for (int i = 0; i < H; ++i)
+                    if (i < heads) po[(int64_t)i * P.Dm] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i]));
             }
         }
         if (u.tiles > 0) {
@@ -747,7 +839,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
     T->abort_flag = 1;
 }
 
-template <int N>
+template <int N, bool kStats>
 __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const __grid_constant__ Params P) {
     using R = Roles<N>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -789,7 +881,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const
     const uint32_t tmem = T->tmem;
 
     if (warp < R::kSoft) {
-        softmax_role<N>(P, smem, T, bars, tmem);
+        softmax_role<N, kStats>(P, smem, T, bars, tmem);
     } else if (warp < R::kGather0) {
         prep_role<N>(P, smem, T, bars);
     } else if (warp < R::kSched) {
@@ -829,20 +921,19 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __g
     if (head0 + h >= P.G || !idx_ok(row, P.rows, P.status)) return;
     const float kInf = __int_as_float(0x7f800000);
     // the unit's pieces: the first starts it (slot 1 of its CTA), the others continue (slot 0)
-    float r = -kInf, m = -kInf;
+    float r = kNoRef, m = -kInf;
     for (int c = c0; c <= c1; ++c) {
         const float *st = P.part_stat + ((int64_t)(2 * c + (c == c0)) * N + h) * 3;
         r = fmaxf(r, st[0]);
         m = fmaxf(m, st[2]);
     }
-    const float rr = fmaxf(r, -1e30f);
     float l = 0.0f;
     float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int c = c0; c <= c1; ++c) {
         const int64_t slot = (int64_t)(2 * c + (c == c0)) * N + h;
         const float *st = P.part_stat + slot * 3;
         if (st[1] == 0.0f) continue;                    // no key of this piece counts
-        const float w = exp2_(fmaxf(st[0], -1e30f) - rr);
+        const float w = exp2_(st[0] - r);
         l = fmaf(st[1], w, l);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -856,7 +947,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __g
             P.out[at * P.Dm + 128 * i + threadIdx.x] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv));
     if (threadIdx.x == 0 && P.smax) {
         P.smax[at] = m > -kInf ? m * kLn2 : m;
-        P.ssum[at] = m > -kInf ? l * exp2_(rr - kShift - m) : l;
+        P.ssum[at] = m > -kInf ? l * exp2_(r - m) : l;
     }
 }
 
@@ -953,8 +1044,9 @@ cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnP
         kern<<<p.grid, threads, kSmemBytes, st>>>(P);
         return cudaGetLastError();
     };
-    cudaError_t e = p.N == 16 ? run(cache_attn_kernel<16>, Roles<16>::kThreads)
-                              : run(cache_attn_kernel<32>, Roles<32>::kThreads);
+    // the statistics cost a maximum per score: a kernel of their own
+    cudaError_t e = p.N == 16 ? run(smax ? cache_attn_kernel<16, true> : cache_attn_kernel<16, false>, Roles<16>::kThreads)
+                              : run(smax ? cache_attn_kernel<32, true> : cache_attn_kernel<32, false>, Roles<32>::kThreads);
     if (e != cudaSuccess || !p.split) return e;
     const dim3 grid((unsigned)p.units, (unsigned)(a.G < 32 ? a.G : 32));
     cache_attn_join_kernel<<<grid, kJoinThreads, 0, st>>>(P, p.N, p.grid);

@@ -5,12 +5,12 @@ With u = 2^-24, D = Dm + Dr, A = max over a row's selected keys of the dot produ
 (scale included), Q = the head's largest |q|, K = max over the keys of scale sum_d |k_d|:
   scores     fp32 sums of exact products of q's parts and the codes (the tensor cores may truncate:
              2 u per term), q held to 2^-22 of Q:         ex = 2 u (D + 8) A + 2^-22 Q K
-  weights    2^(y - ref + 5) with |y| <= A log2(e) + |log2 descale| rounded a few times:
+  weights    2^(y - ref) with |y| <= A log2(e) + |log2 descale| rounded a few times:
              ey = 2^-21 (A + max |log2 descale| + 8); held to 2^-9 relative in two E4M3 parts, and
              never better than 2^-14 in units where the row's largest is at least 2^5: 2^-19 of it
   softmax_max   ex + ey;   softmax_sum / l:  2 (ex + ey) + (n + 8) 2 u
   out        half a step of bf16 of the value, and over E = sum p |k| / l:
-             (2^-9 + 2 (ex + ey) + (n + 8) 4 u) E + n 2^-19 max(p descale) 448 / l
+             (2^-9 + 2 (ex + ey) + (n + 8) 4 u) E + n 2^-18 max(p descale) 448 / l
 """
 import math
 from dataclasses import dataclass
@@ -123,7 +123,7 @@ def check(p, out, smax=None, ssum=None, rows=None, label=""):
         o = (w @ k) / l
         E = (w @ k.abs()) / l
         tol = o.abs() * 2.0 ** -9 + (2.0 ** -9 + 2 * (ex + ey) + (n + 8) * 4 * u) * E + \
-            n * 2.0 ** -19 * 448 * (w * desc[at]).amax(-1, keepdim=True) / l
+            n * 2.0 ** -18 * 448 * (w * desc[at]).amax(-1, keepdim=True) / l
         off = (out[r] - o).abs()
         bad = (off > tol).nonzero()
         assert bad.numel() == 0, (f"{where}: out off by {off.max():.3g} (tolerance there {tol[off == off.max()].max():.3g}) "
