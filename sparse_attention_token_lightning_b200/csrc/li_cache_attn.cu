@@ -26,8 +26,9 @@
 //             maxima reduced and O rescaled. Weights below 2^-18 of the largest may round to 0
 //   prep      the next unit's q: normalised, split and stored in the MMA layout
 //   gather    looks up each selected key's cache row, keeps its scale for the softmax warps and
-//             copies codes and rope part with cp.async into 16 KB slots (128 keys x 128 bytes,
-//             128-byte swizzle; rows that select nothing are zero-filled)
+//             has TMA gather codes and rope part, four rows an instruction, into 16 KB slots (128
+//             keys x 128 bytes, 128-byte swizzle); an entry that selects nothing is row -1, which
+//             reads as zeros
 //   scheduler the CTA's units;  qk / pv: one thread each issues the two products
 // Every wait is bounded in time; on expiry the kernel records LI_DEVERR_TIMEOUT and returns. The
 // softmax warps of a group agree on giving up (the vote carries it), so none is left at a barrier.
@@ -148,9 +149,21 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// 16-byte copy, `bytes` (0 or 16) of them read and the rest filled with zeros.
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// One lane of the warp, chosen by the hardware (all lanes call).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// Four rows of a [rows][x] map, 128 bytes of each from column x on, to four 128-byte rows of shared
+// memory; rows outside the map (-1) read as zeros.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x,
+                                            int32_t r0, int32_t r1, int32_t r2, int32_t r3) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+        : "memory");
 }
 __device__ __forceinline__ float exp2_(float x) {
     float y;
@@ -405,14 +418,11 @@ __device__ __forceinline__ int32_t row_of(const Params &P, int64_t b, int32_t v,
 }
 
 template <int N>
-__device__ void gather_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bars) {
+__device__ void gather_role(const Params &P, const CUtensorMap *tm_codes, const CUtensorMap *tm_rope,
+                            uint8_t *smem, Tail *T, const Bars &bars) {
     const int w = (threadIdx.x >> 5) - Roles<N>::kGather0, lane = threadIdx.x & 31;
-    const int piece = lane & 7, sub = lane >> 3;            // this lane copies keys 32 w + sub + 4 i
-    const uint32_t slots = smem_u32(smem) + P.slot_off;
-    const int key0 = 32 * w + sub;
-    // 16-byte piece of row key in a swizzled slot; key & 7 is sub + 4 (i & 1)
-    const uint32_t dst0 = (uint32_t)(key0 * 128 + ((piece ^ sub) << 4));
-    const uint32_t dst1 = (uint32_t)(key0 * 128 + ((piece ^ (sub + 4)) << 4));
+    const uint32_t dst = smem_u32(smem) + P.slot_off + 32 * w * 128;    // this warp's 32 keys of a slot
+    const uint32_t bytes = (uint32_t)(P.blocks + P.has_rope) * 32u * 128u;
     Ring sr, tr;
     uint32_t err = 0;
     bool ok = true;
@@ -432,32 +442,25 @@ __device__ void gather_role(const Params &P, uint8_t *smem, Tail *T, const Bars 
         if (mine >= 0 && !idx_ok(mine, P.key_rows, P.status)) mine = -1;
         float d = mine >= 0 ? __ldg(P.descale + mine) : 0.0f;
         for (int j = 0; j < u.tiles; ++j, tr.next(kTileRing)) {
-            int32_t row[8];
+            int32_t row[32];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) row[i] = __shfl_sync(0xffffffffu, mine, sub + 4 * i);
-            if (P.has_rope) {
+            for (int i = 0; i < 32; ++i) row[i] = __shfl_sync(0xffffffffu, mine, i);
+            const uint32_t full = bars.tile_full(tr.idx);
+            if (elect_one()) mbar_arrive_expect_tx(full, bytes);
+            __syncwarp();
+            for (int c = P.has_rope ? -1 : 0; c < P.blocks; ++c, sr.next(P.slots)) {
                 if (!wait_warp(bars.slot_empty(sr.idx), sr.phase ^ 1u, &T->abort_flag)) { ok = false; break; }
-                const uint32_t base = slots + sr.idx * kSlot;
+                const uint32_t to = dst + sr.idx * kSlot;
+                const CUtensorMap *map = c < 0 ? tm_rope : tm_codes;
+                const int32_t x = c < 0 ? 0 : 128 * c;
+                if (elect_one()) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int64_t r = row[i] < 0 ? 0 : row[i];
-                    cp_async16_zfill(base + i * 512 + (i & 1 ? dst1 : dst0), P.k_rope + r * 64 + piece * 8,
-                                     row[i] < 0 ? 0u : 16u);
+                    for (int i = 0; i < 8; ++i)
+                        tma_gather4(to + i * 512, map, full, x, row[4 * i], row[4 * i + 1], row[4 * i + 2], row[4 * i + 3]);
                 }
-                sr.next(P.slots);
-            }
-            for (int c = 0; c < P.blocks; ++c, sr.next(P.slots)) {
-                if (!wait_warp(bars.slot_empty(sr.idx), sr.phase ^ 1u, &T->abort_flag)) { ok = false; break; }
-                const uint32_t base = slots + sr.idx * kSlot;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int64_t r = row[i] < 0 ? 0 : row[i];
-                    cp_async16_zfill(base + i * 512 + (i & 1 ? dst1 : dst0),
-                                     P.codes + r * P.Dm + c * 128 + piece * 16, row[i] < 0 ? 0u : 16u);
-                }
+                __syncwarp();
             }
             if (!ok) break;
-            cp_async_arrive(bars.tile_full(tr.idx));
             // a scale outside the range counts as no key: its codes meet weight 0
             if (mine >= 0 && !(d >= kMinDescale && d <= kMaxDescale)) {
                 err |= LI_DEVERR_DESCALE;
@@ -474,9 +477,13 @@ __device__ void gather_role(const Params &P, uint8_t *smem, Tail *T, const Bars 
             v2 = entry_at(P, ir, pos + 2 * kKeys, end);
         }
     }
-    // no copy may still be writing shared memory when the CTA leaves
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if (!ok) T->abort_flag = 1;
+    if (!ok) {
+        T->abort_flag = 1;
+        // copies of a tile that was not issued whole have no barrier to wait on: they land within
+        // microseconds, so the CTA stays for a hundred of them before it gives its memory up
+        const unsigned long long t0 = globaltimer();
+        while (globaltimer() - t0 < 100000ull) {}
+    }
     if (err && P.status) atomicOr(P.status, err);
 }
 
@@ -506,7 +513,6 @@ __device__ void qk_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
             ok = mbar_wait(bars.s_empty(b), ((kt >> 1) & 1u) ^ 1u, &T->abort_flag) &&
                  mbar_wait(bars.tile_full(tr.idx), tr.phase, &T->abort_flag);
             if (!ok) break;
-            fence_async_smem();
             tc_fence_after();
             const uint32_t d = tmem + b * kSCols<N>;
             if (P.has_rope) {
@@ -840,7 +846,9 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
 }
 
 template <int N, bool kStats>
-__global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(
+    const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_rope,
+    const __grid_constant__ Params P) {
     using R = Roles<N>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -864,11 +872,13 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const
         mbar_init(bars.o_done(), 1);
         mbar_init(bars.o_empty(), R::kSoft);
         for (int i = 0; i < kTileRing; ++i) {
-            mbar_init(bars.tile_full(i), 32 * kGatherWarps);
+            mbar_init(bars.tile_full(i), kGatherWarps);
             mbar_init(bars.meta_full(i), 32 * kGatherWarps);
         }
         for (int i = 0; i < kMaxSlots; ++i) mbar_init(bars.slot_empty(i), 1);
         T->abort_flag = 0;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_codes)) : "memory");
+        if (P.has_rope) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_rope)) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == R::kQk) {
@@ -885,7 +895,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const
     } else if (warp < R::kGather0) {
         prep_role<N>(P, smem, T, bars);
     } else if (warp < R::kSched) {
-        gather_role<N>(P, smem, T, bars);
+        gather_role<N>(P, &tm_codes, &tm_rope, smem, T, bars);
     } else if (warp == R::kSched) {
         scheduler_role(P, T, bars);
     } else if (warp == R::kQk) {
@@ -949,6 +959,19 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __g
         P.smax[at] = m > -kInf ? m * kLn2 : m;
         P.ssum[at] = m > -kInf ? l * exp2_(r - m) : l;
     }
+}
+
+// [rows][cols] map for tile::gather4: a box of 128 bytes of one row, 128-byte swizzle.
+bool make_row_map(CUtensorMap *m, const void *ptr, CUtensorMapDataType type, int elem, uint64_t rows, uint64_t cols) {
+    auto fn = encode_fn();
+    if (!fn || rows == 0) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)cols * elem};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / elem), 1u};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, type, 2, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -1038,10 +1061,17 @@ cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnP
     P.p_off = p.p_off;
     P.slot_off = p.slot_off;
     P.tmem_cols = p.tmem_cols;
+    CUtensorMap tm_codes, tm_rope;
+    if (!make_row_map(&tm_codes, a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, P.key_rows, a.Dm)) return cudaErrorInvalidValue;
+    if (a.Dr > 0) {
+        if (!make_row_map(&tm_rope, a.k_rope, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, P.key_rows, 64)) return cudaErrorInvalidValue;
+    } else {
+        tm_rope = tm_codes;
+    }
     auto run = [&](auto kern, int threads) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         if (e != cudaSuccess) return e;
-        kern<<<p.grid, threads, kSmemBytes, st>>>(P);
+        kern<<<p.grid, threads, kSmemBytes, st>>>(tm_codes, tm_rope, P);
         return cudaGetLastError();
     };
     // the statistics cost a maximum per score: a kernel of their own
