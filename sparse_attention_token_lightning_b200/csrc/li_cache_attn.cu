@@ -90,11 +90,11 @@ struct Bars {
     __device__ uint32_t p_empty(int i) const { return at(14 + i); }
     __device__ uint32_t o_done() const { return at(16); }
     __device__ uint32_t o_empty() const { return at(17); }
-    __device__ uint32_t tile_full(int i) const { return at(18 + i); }
-    __device__ uint32_t meta_full(int i) const { return at(18 + kTileRing + i); }
-    __device__ uint32_t slot_empty(int i) const { return at(18 + 2 * kTileRing + i); }
+    __device__ uint32_t meta_full(int i) const { return at(18 + i); }
+    __device__ uint32_t slot_full(int i) const { return at(18 + kTileRing + i); }
+    __device__ uint32_t slot_empty(int i) const { return at(18 + kTileRing + kMaxSlots + i); }
 };
-constexpr int kNumBars = 18 + 2 * kTileRing + kMaxSlots;
+constexpr int kNumBars = 18 + kTileRing + 2 * kMaxSlots;
 struct Tail {
     uint64_t bars[kNumBars];
     Unit unit[2];
@@ -306,14 +306,6 @@ __device__ __forceinline__ bool take_unit(Tail *T, const Bars &bars, int it, Uni
     if ((threadIdx.x & 31) == 0) mbar_arrive(bars.u_empty(it & 1));
     return true;
 }
-// The same for a role of one thread.
-__device__ __forceinline__ bool take_unit_thread(Tail *T, const Bars &bars, int it, Unit *u) {
-    if (!mbar_wait(bars.u_full(it & 1), (it >> 1) & 1, &T->abort_flag)) return false;
-    *u = T->unit[it & 1];
-    mbar_arrive(bars.u_empty(it & 1));
-    return true;
-}
-
 // ---- q: normalised and split ---------------------------------------------------------------------
 template <int N>
 __device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bars) {
@@ -331,58 +323,72 @@ __device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &b
         uint8_t *qb = smem + qr.idx * P.q_bytes;
         uint8_t *rb = qb + P.blocks * (2 * N * 128);
         const int heads = min(P.G - u.head0, N);
-        for (int h = wp; h < N; h += R::kPrep) {
-            const bool real = h < heads;
-            const int64_t qrow = (int64_t)u.row * P.G + u.head0 + (real ? h : 0);
-            uint4 v[2];
-            float amax = 0.0f;
+        for (int h0 = wp; h0 < N; h0 += 4 * R::kPrep) {
+            // four heads of the warp at once, so that their reads overlap
+            uint4 v[4][2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int vec = lane + 32 * i;          // 8 elements
-                v[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (real && vec * 8 < P.Dm && idx_ok(qrow * P.Dm + vec * 8, (int64_t)P.rows * P.G * P.Dm, P.status))
-                    v[i] = __ldg(reinterpret_cast<const uint4 *>(P.q + qrow * P.Dm) + vec);
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            for (int t = 0; t < 4; ++t) {
+                const int h = h0 + t * R::kPrep;
+                const int64_t qrow = (int64_t)u.row * P.G + u.head0 + h;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float a = fabsf(bf16_lo(w[j])), b = fabsf(bf16_hi(w[j]));
-                    if (a < kInf) amax = fmaxf(amax, a);
-                    if (b < kInf) amax = fmaxf(amax, b);
+                for (int i = 0; i < 2; ++i) {
+                    const int vec = lane + 32 * i;          // 8 elements
+                    v[t][i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (h < heads && vec * 8 < P.Dm && idx_ok(qrow * P.Dm + vec * 8, (int64_t)P.rows * P.G * P.Dm, P.status))
+                        v[t][i] = __ldg(reinterpret_cast<const uint4 *>(P.q + qrow * P.Dm) + vec);
                 }
             }
-            amax = warp_max(amax);
-            // f = 2^(7 - exponent of amax): the largest element lands in [128, 256)
-            const int e = max((int)(__float_as_uint(amax) >> 23), 8);   // biased; 8 keeps f finite
-            const float f = amax > 0.0f ? __uint_as_float((uint32_t)(127 + 7 + 127 - e) << 23) : 1.0f;
-            if (lane == 0) T->ah[n & (kAhRing - 1)][h] = P.scale * kLog2e / f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int vec = lane + 32 * i;
-                if (vec * 8 >= P.Dm) continue;
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    // an infinity has no code: NaN, so that the head's result shows it
-                    float a = bf16_lo(w[j]) * f, b = bf16_hi(w[j]) * f;
-                    if (!(fabsf(a) < kInf)) a = __int_as_float(0x7fc00000);
-                    if (!(fabsf(b) < kInf)) b = __int_as_float(0x7fc00000);
-                    hi[j] = e4m3x2(a, b);
-                    const float2 r = e4m3x2_f32(hi[j]);
-                    lo[j] = e4m3x2((a - r.x) * 16.0f, (b - r.y) * 16.0f);
-                }
-                const int off = (vec * 8) & 127, b = vec >> 4;
-                const uint32_t at = (uint32_t)(b * 2 * N * 128 + (((off >> 4) ^ (h & 7)) << 4) + (off & 8));
-                *reinterpret_cast<uint2 *>(qb + at + h * 128) =
-                    make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-                *reinterpret_cast<uint2 *>(qb + at + (N + h) * 128) =
-                    make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-            }
-            if (P.has_rope && lane < 8) {
+            // the rope parts: 8 lanes a head
+            if (P.has_rope) {
+                const int h = h0 + (lane >> 3) * R::kPrep, piece = lane & 7;
+                const int64_t qrow = (int64_t)u.row * P.G + u.head0 + h;
                 uint4 r = make_uint4(0u, 0u, 0u, 0u);
-                if (real && idx_ok(qrow * 64 + lane * 8, (int64_t)P.rows * P.G * 64, P.status))
-                    r = __ldg(reinterpret_cast<const uint4 *>(P.q_rope + qrow * 64) + lane);
-                *reinterpret_cast<uint4 *>(rb + h * 128 + ((lane ^ (h & 7)) << 4)) = r;
+                if (h < heads && idx_ok(qrow * 64 + piece * 8, (int64_t)P.rows * P.G * 64, P.status))
+                    r = __ldg(reinterpret_cast<const uint4 *>(P.q_rope + qrow * 64) + piece);
+                *reinterpret_cast<uint4 *>(rb + h * 128 + ((piece ^ (h & 7)) << 4)) = r;
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int h = h0 + t * R::kPrep;
+                float amax = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t w[4] = {v[t][i].x, v[t][i].y, v[t][i].z, v[t][i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float a = fabsf(bf16_lo(w[j])), b = fabsf(bf16_hi(w[j]));
+                        if (a < kInf) amax = fmaxf(amax, a);
+                        if (b < kInf) amax = fmaxf(amax, b);
+                    }
+                }
+                amax = warp_max(amax);
+                // f = 2^(7 - exponent of amax): the largest element lands in [128, 256)
+                const int e = max((int)(__float_as_uint(amax) >> 23), 8);   // biased; 8 keeps f finite
+                const float f = amax > 0.0f ? __uint_as_float((uint32_t)(127 + 7 + 127 - e) << 23) : 1.0f;
+                if (lane == 0) T->ah[n & (kAhRing - 1)][h] = P.scale * kLog2e / f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int vec = lane + 32 * i;
+                    if (vec * 8 >= P.Dm) continue;
+                    const uint32_t w[4] = {v[t][i].x, v[t][i].y, v[t][i].z, v[t][i].w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        // an infinity has no code: NaN, so that the head's result shows it
+                        float a = bf16_lo(w[j]) * f, b = bf16_hi(w[j]) * f;
+                        if (!(fabsf(a) < kInf)) a = __int_as_float(0x7fc00000);
+                        if (!(fabsf(b) < kInf)) b = __int_as_float(0x7fc00000);
+                        hi[j] = e4m3x2(a, b);
+                        const float2 r = e4m3x2_f32(hi[j]);
+                        lo[j] = e4m3x2((a - r.x) * 16.0f, (b - r.y) * 16.0f);
+                    }
+                    const int off = (vec * 8) & 127, b = vec >> 4;
+                    const uint32_t at = (uint32_t)(b * 2 * N * 128 + (((off >> 4) ^ (h & 7)) << 4) + (off & 8));
+                    *reinterpret_cast<uint2 *>(qb + at + h * 128) =
+                        make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                    *reinterpret_cast<uint2 *>(qb + at + (N + h) * 128) =
+                        make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+                }
             }
         }
         fence_async_smem();
@@ -422,7 +428,6 @@ __device__ void gather_role(const Params &P, const CUtensorMap *tm_codes, const 
                             uint8_t *smem, Tail *T, const Bars &bars) {
     const int w = (threadIdx.x >> 5) - Roles<N>::kGather0, lane = threadIdx.x & 31;
     const uint32_t dst = smem_u32(smem) + P.slot_off + 32 * w * 128;    // this warp's 32 keys of a slot
-    const uint32_t bytes = (uint32_t)(P.blocks + P.has_rope) * 32u * 128u;
     Ring sr, tr;
     uint32_t err = 0;
     bool ok = true;
@@ -445,15 +450,13 @@ __device__ void gather_role(const Params &P, const CUtensorMap *tm_codes, const 
             int32_t row[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) row[i] = __shfl_sync(0xffffffffu, mine, i);
-            const uint32_t full = bars.tile_full(tr.idx);
-            if (elect_one()) mbar_arrive_expect_tx(full, bytes);
-            __syncwarp();
             for (int c = P.has_rope ? -1 : 0; c < P.blocks; ++c, sr.next(P.slots)) {
                 if (!wait_warp(bars.slot_empty(sr.idx), sr.phase ^ 1u, &T->abort_flag)) { ok = false; break; }
-                const uint32_t to = dst + sr.idx * kSlot;
+                const uint32_t to = dst + sr.idx * kSlot, full = bars.slot_full(sr.idx);
                 const CUtensorMap *map = c < 0 ? tm_rope : tm_codes;
                 const int32_t x = c < 0 ? 0 : 128 * c;
                 if (elect_one()) {
+                    mbar_arrive_expect_tx(full, 32u * 128u);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         tma_gather4(to + i * 512, map, full, x, row[4 * i], row[4 * i + 1], row[4 * i + 2], row[4 * i + 3]);
@@ -498,41 +501,44 @@ __device__ void qk_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
     constexpr uint32_t kQBlock = 2 * N * 128;
     constexpr uint32_t idesc8 = (1u << 4) | ((2u * N >> 3) << 17) | (8u << 24);
     constexpr uint32_t idesc16 = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
-    Ring qr, sr, tr;
+    Ring qr, sr;
     uint32_t kt = 0;
     for (int it = 0;; ++it) {
         Unit u;
-        if (!take_unit_thread(T, bars, it, &u)) break;
-        if (u.row < 0) return;
-        if (u.tiles == 0) continue;
-        if (!mbar_wait(bars.q_full(qr.idx), qr.phase, &T->abort_flag)) break;
+        if (!take_unit(T, bars, it, &u)) break;
+        const int tiles = __shfl_sync(0xffffffffu, u.row < 0 ? -1 : u.tiles, 0);
+        if (tiles < 0) return;
+        if (tiles == 0) continue;
+        if (!wait_warp(bars.q_full(qr.idx), qr.phase, &T->abort_flag)) break;
         const uint32_t qa = sbase + qr.idx * P.q_bytes;
         bool ok = true;
-        for (int j = 0; j < u.tiles; ++j, ++kt, tr.next(kTileRing)) {
-            const uint32_t b = kt & 1u;
-            ok = mbar_wait(bars.s_empty(b), ((kt >> 1) & 1u) ^ 1u, &T->abort_flag) &&
-                 mbar_wait(bars.tile_full(tr.idx), tr.phase, &T->abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t d = tmem + b * kSCols<N>;
-            if (P.has_rope) {
+        for (int j = 0; j < tiles && ok; ++j, ++kt) {
+            const uint32_t b = kt & 1u, d = tmem + b * kSCols<N>;
+            ok = wait_warp(bars.s_empty(b), ((kt >> 1) & 1u) ^ 1u, &T->abort_flag);
+            // a slot's part of the product starts when the slot is there; the rope part comes first
+            for (int c = P.has_rope ? -1 : 0; c < P.blocks && ok; ++c, sr.next(P.slots)) {
+                ok = wait_warp(bars.slot_full(sr.idx), sr.phase, &T->abort_flag);
+                if (!ok) break;
+                tc_fence_after();
                 const uint64_t a = sw128_desc(slots + sr.idx * kSlot);
-                const uint64_t q = sw128_desc(qa + P.blocks * kQBlock);
+                const uint64_t q = sw128_desc(qa + (c < 0 ? P.blocks : c) * kQBlock);
+                if (elect_one()) {
+                    if (c < 0) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) umma_f16(d + 2 * N, a + 2 * k, q + 2 * k, idesc16, k > 0);
-                umma_commit(bars.slot_empty(sr.idx));
-                sr.next(P.slots);
-            }
-            for (int c = 0; c < P.blocks; ++c, sr.next(P.slots)) {
-                const uint64_t a = sw128_desc(slots + sr.idx * kSlot);
-                const uint64_t q = sw128_desc(qa + c * kQBlock);
+                        for (int k = 0; k < 4; ++k) umma_f16(d + 2 * N, a + 2 * k, q + 2 * k, idesc16, k > 0);
+                        umma_commit(bars.slot_empty(sr.idx));
+                    } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) umma_f8(d, a + 2 * k, q + 2 * k, idesc8, (c | k) != 0);
+                        for (int k = 0; k < 4; ++k) umma_f8(d, a + 2 * k, q + 2 * k, idesc8, (c | k) != 0);
+                        if (c == P.blocks - 1) umma_commit(bars.s_full(b));
+                    }
+                }
+                __syncwarp();
             }
-            umma_commit(bars.s_full(b));
         }
         if (!ok) break;
-        umma_commit(bars.q_empty(qr.idx));
+        if (elect_one()) umma_commit(bars.q_empty(qr.idx));
+        __syncwarp();
         qr.next(P.q_bufs);
     }
     T->abort_flag = 1;
@@ -546,29 +552,35 @@ __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
     uint32_t kt = 0, nu = 0;
     for (int it = 0;; ++it) {
         Unit u;
-        if (!take_unit_thread(T, bars, it, &u)) break;
-        if (u.row < 0) return;
-        if (u.tiles == 0) continue;
+        if (!take_unit(T, bars, it, &u)) break;
+        const int tiles = __shfl_sync(0xffffffffu, u.row < 0 ? -1 : u.tiles, 0);
+        if (tiles < 0) return;
+        if (tiles == 0) continue;
         bool ok = true;
-        for (int j = 0; j < u.tiles; ++j, ++kt) {
+        for (int j = 0; j < tiles; ++j, ++kt) {
             // the unit's first product overwrites O: the unit before must have been read out
-            ok = (j > 0 || nu == 0 || mbar_wait(bars.o_empty(), (nu - 1) & 1u, &T->abort_flag)) &&
-                 mbar_wait(bars.p_full(kt & 1u), (kt >> 1) & 1u, &T->abort_flag);
+            ok = (j > 0 || nu == 0 || wait_warp(bars.o_empty(), (nu - 1) & 1u, &T->abort_flag)) &&
+                 wait_warp(bars.p_full(kt & 1u), (kt >> 1) & 1u, &T->abort_flag);
             if (!ok) break;
-            fence_async_smem();
+            fence_async_smem();                 // the weights, for the async proxy
             tc_fence_after();
             const uint64_t p = weights_desc<N>(sbase + P.p_off + (kt & 1u) * (2 * N * 128));
             if (P.has_rope) sr.next(P.slots);
             for (int c = 0; c < P.blocks; ++c, sr.next(P.slots)) {
-                const uint32_t va = slots + sr.idx * kSlot;
+                const uint64_t v = sw128_desc_mn(slots + sr.idx * kSlot, kSlot);
                 const uint32_t d = tmem + 2 * kSCols<N> + c * 2 * N;
+                if (elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    umma_f8(d, sw128_desc_mn(va + k * 32 * 128, kSlot), p + k * (32 * 2 * N >> 4), idesc, (j | k) != 0);
-                umma_commit(bars.slot_empty(sr.idx));
+                    for (int k = 0; k < 4; ++k)
+                        umma_f8(d, v + k * (32 * 128 >> 4), p + k * (32 * 2 * N >> 4), idesc, (j | k) != 0);
+                    umma_commit(bars.slot_empty(sr.idx));
+                    if (c == P.blocks - 1) {
+                        umma_commit(bars.p_empty(kt & 1u));
+                        umma_commit(bars.o_done());
+                    }
+                }
+                __syncwarp();
             }
-            umma_commit(bars.p_empty(kt & 1u));
-            umma_commit(bars.o_done());
         }
         if (!ok) break;
         ++nu;
@@ -807,11 +819,12 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 P.ssum[head_at + lane] = m > -kInf ? s * exp2_(r - m) : s;
             }
         }
-        for (int c = 0; c < P.blocks; ++c) {
-            float o[H];
-#pragma unroll
-            for (int i = 0; i < H; ++i) o[i] = 0.0f;
-            if (u.tiles > 0) {
+        // O out of TMEM, whole units as bf16 (two heads a register), so that the next unit's product
+        // can start before the stores
+        if (u.part >= 0) {
+            float *po = P.part_o + ((int64_t)u.part * N + H * g) * P.Dm + key;
+            // a piece without keys is told by its sum of 0; nothing else of it is read
+            for (int c = 0; c < P.blocks && u.tiles > 0; ++c) {
                 uint32_t hi[H], lo[H];
                 const uint32_t at = tmem + lanes + 2 * kSCols<N> + c * 2 * N + H * g;
                 tmem_ld_nowait(at, hi);
@@ -819,26 +832,53 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < H; ++i)
-                    o[i] = l[i] * fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
+                    if (i < heads && row_ok)
+                        po[(int64_t)i * P.Dm + 128 * c] = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
             }
-            if (!row_ok) continue;
-            if (u.part >= 0) {
-                if (u.tiles == 0) continue;             // its sum of 0 says that nothing is there
-                float *po = P.part_o + ((int64_t)u.part * N + H * g) * P.Dm + 128 * c + key;
-#pragma unroll
-                for (int i = 0; i < H; ++i)
-                    if (i < heads) po[(int64_t)i * P.Dm] = o[i];
-            } else {
-                uint16_t *po = P.out + head_at * P.Dm + 128 * c + key;
-#pragma unroll
-                for (int i = 0; i < H; ++i)
-                    if (i < heads) po[(int64_t)i * P.Dm] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i]));
+            if (u.tiles > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars.o_empty());
             }
-        }
-        if (u.tiles > 0) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars.o_empty());
+        } else {
+            uint32_t o[4][H / 2];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                for (int i = 0; i < H / 2; ++i) o[c][i] = 0u;
+                if (c < P.blocks && u.tiles > 0) {
+                    uint32_t hi[H], lo[H];
+                    const uint32_t at = tmem + lanes + 2 * kSCols<N> + c * 2 * N + H * g;
+                    tmem_ld_nowait(at, hi);
+                    tmem_ld_nowait(at + N, lo);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < H; i += 2) {
+                        const float a = l[i] * fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
+                        const float b = l[i + 1] * fmaf(__uint_as_float(lo[i + 1]), 0.0625f, __uint_as_float(hi[i + 1]));
+                        const __nv_bfloat162 ab = __floats2bfloat162_rn(a, b);
+                        o[c][i / 2] = *reinterpret_cast<const uint32_t *>(&ab);
+                    }
+                }
+            }
+            if (u.tiles > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars.o_empty());
+            }
+            // neighbouring lanes exchange halves: an even lane stores two dims of the even heads, an
+            // odd lane of the odd heads
+            uint16_t *po = P.out + head_at * P.Dm + (key & ~1) + (int64_t)(lane & 1) * P.Dm;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                for (int i = 0; i < H / 2; ++i) {
+                    const uint32_t mine = o[c][i], theirs = __shfl_xor_sync(0xffffffffu, mine, 1);
+                    const uint32_t v = lane & 1 ? __byte_perm(theirs, mine, 0x7632) : __byte_perm(mine, theirs, 0x5410);
+                    if (c < P.blocks && 2 * i + (lane & 1) < heads && row_ok)
+                        *reinterpret_cast<uint32_t *>(po + (int64_t)(2 * i) * P.Dm + 128 * c) = v;
+                }
+            }
         }
         named_bar(bar_id, 128);         // sums, maxima and references are read before they are reset
     }
@@ -851,7 +891,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(
     const __grid_constant__ Params P) {
     using R = Roles<N>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     if (smem_u32(smem) & 1023u) {
         if (threadIdx.x == 0 && P.status) atomicOr(P.status, kDevErrInternal);
         return;
@@ -871,11 +911,11 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(
         }
         mbar_init(bars.o_done(), 1);
         mbar_init(bars.o_empty(), R::kSoft);
-        for (int i = 0; i < kTileRing; ++i) {
-            mbar_init(bars.tile_full(i), kGatherWarps);
-            mbar_init(bars.meta_full(i), 32 * kGatherWarps);
+        for (int i = 0; i < kTileRing; ++i) mbar_init(bars.meta_full(i), 32 * kGatherWarps);
+        for (int i = 0; i < kMaxSlots; ++i) {
+            mbar_init(bars.slot_full(i), kGatherWarps);
+            mbar_init(bars.slot_empty(i), 1);
         }
-        for (int i = 0; i < kMaxSlots; ++i) mbar_init(bars.slot_empty(i), 1);
         T->abort_flag = 0;
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_codes)) : "memory");
         if (P.has_rope) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_rope)) : "memory");
@@ -899,11 +939,9 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(
     } else if (warp == R::kSched) {
         scheduler_role(P, T, bars);
     } else if (warp == R::kQk) {
-        if (lane == 0) qk_role<N>(P, smem, T, bars, tmem);
-        __syncwarp();
+        qk_role<N>(P, smem, T, bars, tmem);
     } else {
-        if (lane == 0) pv_role<N>(P, smem, T, bars, tmem);
-        __syncwarp();
+        pv_role<N>(P, smem, T, bars, tmem);
     }
 
     tc_fence_before();
