@@ -19,6 +19,26 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kMinScale = 8.077935669463161e-28f;     // 2^-90
 
+// Division of a non-negative int32 by a fixed one (Granlund and Montgomery, "Division by invariant
+// integers using multiplication", 1994): with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1,
+// t / d = (h + ((t - h) >> 1)) >> (l - 1) for h = floor(m t / 2^32); d = 1 apart.
+struct FixedDiv {
+    uint32_t m = 0;
+    int32_t shift = -1;                 // l - 1, -1 for d = 1
+    __host__ explicit FixedDiv(uint32_t d = 1) {
+        if (d <= 1) return;
+        int l = 0;
+        while (((uint64_t)1 << l) < d) ++l;
+        m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1);
+        shift = l - 1;
+    }
+    __device__ __forceinline__ int32_t div(int32_t t) const {
+        if (shift < 0) return t;
+        const uint32_t h = __umulhi(m, (uint32_t)t);
+        return (int32_t)((h + (((uint32_t)t - h) >> 1)) >> shift);
+    }
+};
+
 struct CacheParams {
     void *x, *rope;
     uint8_t *codes;
@@ -31,75 +51,67 @@ struct CacheParams {
     int32_t rows, batch, x_len, k_len, num_blocks, block_size;
     int32_t dim, rope_dim;
     int32_t paged, lanes, lanes_log2;           // lanes per row
+    FixedDiv by_len, by_block;                  // x_len, block_size
 };
 
 __device__ __forceinline__ void report(const CacheParams &P, uint32_t bits) {
     if (bits && P.status) atomicOr(P.status, bits);
 }
 
-// Where row r of the call sits: its batch and position inside it, and its cache row; false when
-// the row takes no part (past the rows in use, or data that does not fit, which is reported).
-struct Place {
-    int64_t x_off, r_off;       // element offsets of the row in x and rope
-    int64_t slot;               // cache row
-};
-__device__ __forceinline__ bool place_row(const CacheParams &P, int32_t r, Place *out) {
+// Element offset of row r of the call in x (or rope), by its strides.
+__device__ __forceinline__ int64_t row_offset(const CacheParams &P, int32_t r, int64_t batch, int64_t row) {
+    if (P.cu_seqlens) return (int64_t)r * row;
+    const int32_t b = P.by_len.div(r);
+    return b * batch + (r - b * P.x_len) * row;
+}
+
+// Cache row of row r of the call, -1 where it takes no part: past the rows in use, or data that does
+// not fit, which is added to *err.
+__device__ __forceinline__ int64_t cache_row(const CacheParams &P, int32_t r, uint32_t *err) {
     int32_t b, i, L1;
-    uint32_t err = 0;
     if (P.cu_seqlens) {
         const int32_t *cu = P.cu_seqlens;
-        if (r < cu[0] || r >= cu[P.batch]) return false;
+        if (r < __ldg(cu) || r >= __ldg(cu + P.batch)) return -1;
         int32_t lo = 0, hi = P.batch;
         while (hi - lo > 1) {
             const int32_t mid = (lo + hi) >> 1;
-            if (cu[mid] <= r) lo = mid; else hi = mid;
+            if (__ldg(cu + mid) <= r) lo = mid; else hi = mid;
         }
         b = lo;
-        i = r - cu[b];
-        L1 = cu[b + 1] - cu[b];
+        const int32_t first = __ldg(cu + b);
+        i = r - first;
+        L1 = __ldg(cu + b + 1) - first;
         if (i < 0 || i >= L1) {                 // only lengths that decrease lead here
-            report(P, LI_DEVERR_LENGTHS);
-            return false;
+            *err |= LI_DEVERR_LENGTHS;
+            return -1;
         }
-        out->x_off = (int64_t)r * P.x_row;
-        out->r_off = (int64_t)r * P.r_row;
     } else {
-        b = r / P.x_len;
+        b = P.by_len.div(r);
         i = r - b * P.x_len;
         L1 = P.x_len;
-        out->x_off = b * P.x_batch + i * P.x_row;
-        out->r_off = b * P.r_batch + i * P.r_row;
-    }
-    if (P.seqused) {
-        const int32_t u = P.seqused[b];
-        if (u < 0 || u > L1) err |= LI_DEVERR_LENGTHS;
-        L1 = min(max(u, 0), L1);
     }
     const int64_t cap = P.paged ? P.bt_stride * P.block_size : P.k_len;
-    int64_t L2 = P.k_len;
-    if (P.seqused_k) {
-        L2 = P.seqused_k[b];
-        if (L2 < 0 || L2 > cap) err |= LI_DEVERR_LENGTHS;
+    int64_t L2 = P.seqused_k ? __ldg(P.seqused_k + b) : P.k_len;
+    if (L2 < 0 || L2 > cap) *err |= LI_DEVERR_LENGTHS;
+    if (P.seqused) {
+        const int32_t u = __ldg(P.seqused + b);
+        if (u < 0 || u > L1) *err |= LI_DEVERR_LENGTHS;
+        L1 = min(max(u, 0), L1);
     }
     const int64_t pos = L2 - L1 + i;
-    bool take = i < L1;
-    if (take && (pos < 0 || pos >= cap)) {
-        err |= LI_DEVERR_LENGTHS;
-        take = false;
+    if (i >= L1) return -1;
+    if (pos < 0 || pos >= cap) {
+        *err |= LI_DEVERR_LENGTHS;
+        return -1;
     }
-    if (take && P.paged) {
-        const int32_t q = (int32_t)pos / P.block_size;         // below the int32 L2
-        const int32_t blk = P.block_table[(int64_t)b * P.bt_stride + q];
-        if (blk < 0 || blk >= P.num_blocks) {
-            err |= LI_DEVERR_TABLE;
-            take = false;
-        }
-        out->slot = (int64_t)blk * P.block_size + ((int32_t)pos - q * P.block_size);
-    } else {
-        out->slot = (int64_t)b * P.k_len + pos;
+    if (!P.paged) return (int64_t)b * P.k_len + pos;
+    const int32_t q = P.by_block.div((int32_t)pos);         // pos is below the int32 L2
+    const int32_t blk = __ldg(P.block_table + (int64_t)b * P.bt_stride + q);
+    if (blk < 0 || blk >= P.num_blocks) {
+        *err |= LI_DEVERR_TABLE;
+        return -1;
     }
-    report(P, err);
-    return take;
+    return (int64_t)blk * P.block_size + ((int32_t)pos - q * P.block_size);
 }
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -112,11 +124,12 @@ template <> __device__ __forceinline__ float from_f32(float v) { return v; }
 
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) < __int_as_float(0x7f800000); }
 
-// E4M3 codes of the exact quotients a / s and b / s; inv = 1 / s. a * inv is within two units in the
-// last place of the quotient, which decides the code unless it lies that near to a border between
-// two codes. Borders have at most 5 significant bits, so the 19 lowest mantissa bits tell; there
-// the quotient is rounded to odd instead (its last bit set when the division leaves a remainder),
-// and the second rounding sees on which side it lies. Powers of two divide exactly.
+// x / s for the conversion to E4M3, which rounds it to nearest, ties to even: x * inv, inv = 1 / s,
+// is within two units in the last place of the quotient, and that decides the code unless a border
+// between two codes is as near. Of codes above 2^-6 a border has bit 19 of the mantissa as its last
+// one; there, and below 2^-6, the quotient is rounded to odd instead (its last bit set when the
+// division leaves a remainder), and the second rounding sees on which side it lies. Powers of two
+// divide exactly.
 __device__ __noinline__ float odd_quotient(float x, float s) {
     const float q = __fdiv_rn(x, s);
     const float rem = fmaf(-q, s, x);
@@ -129,12 +142,10 @@ template <bool kPow2>
 __device__ __forceinline__ float quotient(float x, float s, float inv) {
     const float q = x * inv;
     if constexpr (!kPow2) {
-        if (((__float_as_int(q) + 4) & 0x7ffff) < 8) return odd_quotient(x, s);
+        if (((__float_as_int(q) + 0x80004) & 0xfffff) < 8 || fabsf(q) < 0.015625f) return odd_quotient(x, s);
     }
     return q;
 }
-// NaN stays NaN; an infinity has no code either.
-__device__ __forceinline__ float coded(float x, float q) { return finite(x) ? q : __int_as_float(0x7fc00000); }
 
 __device__ __forceinline__ float row_scale(float amax, bool pow2) {
     if (!(amax > 0.0f)) return 1.0f;
@@ -144,117 +155,162 @@ __device__ __forceinline__ float row_scale(float amax, bool pow2) {
     return __int_as_float(max(e - 8, 127 - 90) << 23);
 }
 
-// Eight elements of T in one or two 16-byte accesses, or element by element.
+// Eight elements of T: one or two 16-byte accesses, or element by element.
+template <class T> struct alignas(16) Eight { T v[8]; };
 template <class T, bool kWide>
-__device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
-    if constexpr (!kWide) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
-    } else {
-        T t[8];
+__device__ __forceinline__ void load8(Eight<T> &e, const T *p) {
+    if constexpr (kWide) {
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-            reinterpret_cast<uint4 *>(t)[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+            reinterpret_cast<uint4 *>(e.v)[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f32(t[i]);
+        for (int i = 0; i < 8; ++i) e.v[i] = p[i];
     }
 }
 template <class T, bool kWide>
-__device__ __forceinline__ void store8(T *p, const float (&v)[8]) {
-    if constexpr (!kWide) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = from_f32<T>(v[i]);
-    } else {
-        T t[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = from_f32<T>(v[i]);
+__device__ __forceinline__ void store8(T *p, const Eight<T> &e) {
+    if constexpr (kWide) {
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-            reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(t)[i];
-    }
-}
-// The rope part of a row: eight elements a lane and step (rope_dim is a multiple of eight).
-template <class T, bool kWide>
-__device__ __forceinline__ void copy_row(T *to, const T *from, int n, int lane, int lanes) {
-    for (int d = 8 * lane; d < n; d += 8 * lanes) {
-        float v[8];
-        load8<T, kWide>(from + d, v);
-        store8<T, kWide>(to + d, v);
+            reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(e.v)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = e.v[i];
     }
 }
 
-// kSteps: steps of eight elements that a lane may take (dim <= 8 lanes kSteps).
+// max(m, |e|) over the eight elements, NaN left out (two 16-bit elements an instruction).
+__device__ __forceinline__ void max8(__nv_bfloat162 &m, const Eight<__nv_bfloat16> &e) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) m = __hmax2(m, __habs2(__nv_bfloat162(e.v[i], e.v[i + 1])));
+}
+__device__ __forceinline__ void max8(__half2 &m, const Eight<__half> &e) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) m = __hmax2(m, __habs2(__half2(e.v[i], e.v[i + 1])));
+}
+__device__ __forceinline__ void max8(float &m, const Eight<float> &e) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(e.v[i]));
+}
+__device__ __forceinline__ float most(__nv_bfloat162 m) { return fmaxf(__low2float(m), __high2float(m)); }
+__device__ __forceinline__ float most(__half2 m) { return fmaxf(__low2float(m), __high2float(m)); }
+__device__ __forceinline__ float most(float m) { return m; }
+template <class T> struct MaxOf { using type = float; };
+template <> struct MaxOf<__nv_bfloat16> { using type = __nv_bfloat162; };
+template <> struct MaxOf<__half> { using type = __half2; };
+
+__device__ __forceinline__ float group_max(float m, int lanes) {
+    for (int o = lanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+
+// A row per group of lanes; kSteps: steps of eight elements that a lane may take (dim <= 8 lanes
+// kSteps). The row is read before its place in the cache is looked up.
 template <class T, bool kWide, bool kPow2, int kSteps>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheParams P) {
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ CacheParams P) {
     const int lane = threadIdx.x & (P.lanes - 1);
     const int64_t r = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> P.lanes_log2;
-    Place at;
-    const bool take = r < P.rows && place_row(P, (int32_t)r, &at);
-    float v[kSteps][8];
-    float amax = 0.0f;
-    if (take) {
-        const T *x = static_cast<const T *>(P.x) + at.x_off;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-            const int d = 8 * (lane + k * P.lanes);
-            if (d < P.dim) load8<T, kWide>(x + d, v[k]);
-        }
+    Eight<T> v[kSteps], rp;
+    int64_t slot = -1;
+    typename MaxOf<T>::type m2{};
+    const T *rope = static_cast<const T *>(P.rope);
+    if (r < P.rows) {
+        const T *x = static_cast<const T *>(P.x) + row_offset(P, (int32_t)r, P.x_batch, P.x_row) + 8 * lane;
 #pragma unroll
         for (int k = 0; k < kSteps; ++k)
-            if (8 * (lane + k * P.lanes) < P.dim)
+            if (8 * (lane + k * P.lanes) < P.dim) load8<T, kWide>(v[k], x + 8 * k * P.lanes);
+        if (8 * lane < P.rope_dim) {
+            rope += row_offset(P, (int32_t)r, P.r_batch, P.r_row) + 8 * lane;
+            load8<T, kWide>(rp, rope);
+        }
+        uint32_t err = 0;
+        slot = cache_row(P, (int32_t)r, &err);
+        report(P, err);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (finite(v[k][i])) amax = fmaxf(amax, fabsf(v[k][i]));
+        for (int k = 0; k < kSteps; ++k)
+            if (8 * (lane + k * P.lanes) < P.dim) max8(m2, v[k]);
     }
-    for (int o = P.lanes / 2; o > 0; o >>= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (!take) return;
+    float amax = group_max(most(m2), P.lanes);
+    // a row with an infinity: once more without it, and no code for it but NaN's
+    const bool inf = !finite(amax);
+    if (__any_sync(0xffffffffu, inf)) {
+        float m = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+            if (inf && 8 * (lane + k * P.lanes) < P.dim)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float t = fabsf(to_f32(v[k].v[i]));
+                    if (finite(t)) m = fmaxf(m, t);
+                    else v[k].v[i] = from_f32<T>(__int_as_float(0x7fc00000));
+                }
+        m = group_max(m, P.lanes);
+        if (inf) amax = m;
+    }
+    if (slot < 0) return;
     const float s = row_scale(amax, kPow2), inv = __frcp_rn(s);
-    if (lane == 0) P.descale[at.slot] = s;
-    uint8_t *codes = P.codes + at.slot * P.dim;
+    if (lane == 0) P.descale[slot] = s;
+    uint8_t *codes = P.codes + slot * P.dim + 8 * lane;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
-        const int d = 8 * (lane + k * P.lanes);
-        if (d >= P.dim) continue;
+        if (8 * (lane + k * P.lanes) >= P.dim) continue;
         uint32_t c[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = v[k][2 * i], b = v[k][2 * i + 1];
-            c[i] = __nv_cvt_float2_to_fp8x2(make_float2(coded(a, quotient<kPow2>(a, s, inv)), coded(b, quotient<kPow2>(b, s, inv))),
+        for (int i = 0; i < 4; ++i)
+            c[i] = __nv_cvt_float2_to_fp8x2(make_float2(quotient<kPow2>(to_f32(v[k].v[2 * i]), s, inv),
+                                                        quotient<kPow2>(to_f32(v[k].v[2 * i + 1]), s, inv)),
                                             __NV_SATFINITE, __NV_E4M3);
-        }
-        *reinterpret_cast<uint2 *>(codes + d) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+        *reinterpret_cast<uint2 *>(codes + 8 * k * P.lanes) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
     }
-    if (P.rope_dim > 0)
-        copy_row<T, kWide>(reinterpret_cast<T *>(P.rope_cache) + at.slot * P.rope_dim,
-                           static_cast<const T *>(P.rope) + at.r_off, P.rope_dim, lane, P.lanes);
+    if (8 * lane >= P.rope_dim) return;
+    T *rc = reinterpret_cast<T *>(P.rope_cache) + slot * P.rope_dim + 8 * lane;
+    store8<T, true>(rc, rp);
+    for (int d = 8 * P.lanes; d + 8 * lane < P.rope_dim; d += 8 * P.lanes) {
+        load8<T, kWide>(rp, rope + d);
+        store8<T, true>(rc + d, rp);
+    }
 }
 
-template <class T, bool kWide>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheParams P) {
+template <class T, bool kWide, int kSteps>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheParams P) {
     const int lane = threadIdx.x & (P.lanes - 1);
     const int64_t r = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> P.lanes_log2;
-    Place at;
-    if (r >= P.rows || !place_row(P, (int32_t)r, &at)) return;
-    T *x = static_cast<T *>(P.x) + at.x_off;
-    const uint8_t *codes = P.codes + at.slot * P.dim;
-    const float s = P.descale[at.slot];
-    for (int d = 8 * lane; d < P.dim; d += 8 * P.lanes) {
-        const uint2 c = *reinterpret_cast<const uint2 *>(codes + d);
-        float v[8];
+    if (r >= P.rows) return;
+    uint32_t err = 0;
+    const int64_t slot = cache_row(P, (int32_t)r, &err);
+    report(P, err);
+    if (slot < 0) return;
+    const float s = __ldg(P.descale + slot);
+    const uint8_t *codes = P.codes + slot * P.dim + 8 * lane;
+    const T *rc = reinterpret_cast<const T *>(P.rope_cache) + slot * P.rope_dim + 8 * lane;
+    uint2 c[kSteps];
+    Eight<T> rp;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+        if (8 * (lane + k * P.lanes) < P.dim) c[k] = __ldcs(reinterpret_cast<const uint2 *>(codes + 8 * k * P.lanes));
+    if (8 * lane < P.rope_dim) load8<T, true>(rp, rc);
+    T *x = static_cast<T *>(P.x) + row_offset(P, (int32_t)r, P.x_batch, P.x_row) + 8 * lane;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+        if (8 * (lane + k * P.lanes) >= P.dim) continue;
+        Eight<T> e;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t w = (i < 2 ? c.x : c.y) >> (16 * (i & 1)) & 0xffffu;
+            const uint32_t w = (i < 2 ? c[k].x : c[k].y) >> (16 * (i & 1)) & 0xffffu;
             const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3)));
-            v[2 * i] = f.x * s;
-            v[2 * i + 1] = f.y * s;
+            e.v[2 * i] = from_f32<T>(f.x * s);
+            e.v[2 * i + 1] = from_f32<T>(f.y * s);
         }
-        store8<T, kWide>(x + d, v);
+        store8<T, kWide>(x + 8 * k * P.lanes, e);
     }
-    if (P.rope_dim > 0)
-        copy_row<T, kWide>(static_cast<T *>(P.rope) + at.r_off,
-                           reinterpret_cast<const T *>(P.rope_cache) + at.slot * P.rope_dim, P.rope_dim,
-                           lane, P.lanes);
+    if (8 * lane >= P.rope_dim) return;
+    T *rope = static_cast<T *>(P.rope) + row_offset(P, (int32_t)r, P.r_batch, P.r_row) + 8 * lane;
+    store8<T, kWide>(rope, rp);
+    for (int d = 8 * P.lanes; d + 8 * lane < P.rope_dim; d += 8 * P.lanes) {
+        load8<T, true>(rp, rc + d);
+        store8<T, kWide>(rope + d, rp);
+    }
 }
 
 CacheParams params(const li_cache_args &a) {
@@ -283,9 +339,13 @@ CacheParams params(const li_cache_args &a) {
     P.dim = a.dim;
     P.rope_dim = a.rope_dim;
     P.paged = a.layout_k == LI_LAYOUT_PA_BSND;
-    P.lanes_log2 = 1;
-    while (P.lanes_log2 < 5 && (8 << P.lanes_log2) < a.dim) ++P.lanes_log2;
+    // two steps of eight elements a lane (three or four where dim / 16 is no power of two or above
+    // 32), so that a row's address work is shared by 16 elements a lane
+    P.lanes_log2 = 0;
+    while (P.lanes_log2 < 5 && (32 << P.lanes_log2) <= a.dim) ++P.lanes_log2;
     P.lanes = 1 << P.lanes_log2;
+    P.by_len = FixedDiv(a.x_len);
+    P.by_block = FixedDiv(P.paged ? a.block_size : 1);
     return P;
 }
 
@@ -304,26 +364,25 @@ unsigned blocks_of(const CacheParams &P) {
     return (unsigned)(((int64_t)P.rows * P.lanes + kThreads - 1) / kThreads);
 }
 
-}  // namespace
-
-namespace {
-
 template <class T, bool kWide, bool kPow2>
-void write_steps(const CacheParams &P, unsigned n, cudaStream_t st) {
-    const int steps = (P.dim + 8 * P.lanes - 1) / (8 * P.lanes);
-    if (steps == 1) cache_write_kernel<T, kWide, kPow2, 1><<<n, kThreads, 0, st>>>(P);
-    else if (steps == 2) cache_write_kernel<T, kWide, kPow2, 2><<<n, kThreads, 0, st>>>(P);
-    else cache_write_kernel<T, kWide, kPow2, 4><<<n, kThreads, 0, st>>>(P);
+void write_steps(const CacheParams &P, cudaStream_t st) {
+    if (P.dim <= 16 * P.lanes) cache_write_kernel<T, kWide, kPow2, 2><<<blocks_of(P), kThreads, 0, st>>>(P);
+    else cache_write_kernel<T, kWide, kPow2, 4><<<blocks_of(P), kThreads, 0, st>>>(P);
 }
 template <class T>
-void write_type(const CacheParams &P, bool wide, bool pow2, unsigned n, cudaStream_t st) {
-    if (wide) pow2 ? write_steps<T, true, true>(P, n, st) : write_steps<T, true, false>(P, n, st);
-    else pow2 ? write_steps<T, false, true>(P, n, st) : write_steps<T, false, false>(P, n, st);
+void write_type(const CacheParams &P, bool wide, bool pow2, cudaStream_t st) {
+    if (wide) pow2 ? write_steps<T, true, true>(P, st) : write_steps<T, true, false>(P, st);
+    else pow2 ? write_steps<T, false, true>(P, st) : write_steps<T, false, false>(P, st);
+}
+template <class T, bool kWide>
+void read_steps(const CacheParams &P, cudaStream_t st) {
+    if (P.dim <= 16 * P.lanes) cache_read_kernel<T, kWide, 2><<<blocks_of(P), kThreads, 0, st>>>(P);
+    else cache_read_kernel<T, kWide, 4><<<blocks_of(P), kThreads, 0, st>>>(P);
 }
 template <class T>
-void read_type(const CacheParams &P, bool wide, unsigned n, cudaStream_t st) {
-    if (wide) cache_read_kernel<T, true><<<n, kThreads, 0, st>>>(P);
-    else cache_read_kernel<T, false><<<n, kThreads, 0, st>>>(P);
+void read_type(const CacheParams &P, bool wide, cudaStream_t st) {
+    if (wide) read_steps<T, true>(P, st);
+    else read_steps<T, false>(P, st);
 }
 
 }  // namespace
@@ -331,18 +390,18 @@ void read_type(const CacheParams &P, bool wide, unsigned n, cudaStream_t st) {
 cudaError_t launch_cache_write(const li_cache_args &a, cudaStream_t st) {
     const CacheParams P = params(a);
     const bool wide = wide_rows(a), pow2 = a.pow2 != 0;
-    if (a.dtype == LI_DTYPE_BF16) write_type<__nv_bfloat16>(P, wide, pow2, blocks_of(P), st);
-    else if (a.dtype == LI_DTYPE_FP16) write_type<__half>(P, wide, pow2, blocks_of(P), st);
-    else write_type<float>(P, wide, pow2, blocks_of(P), st);
+    if (a.dtype == LI_DTYPE_BF16) write_type<__nv_bfloat16>(P, wide, pow2, st);
+    else if (a.dtype == LI_DTYPE_FP16) write_type<__half>(P, wide, pow2, st);
+    else write_type<float>(P, wide, pow2, st);
     return cudaGetLastError();
 }
 
 cudaError_t launch_cache_read(const li_cache_args &a, cudaStream_t st) {
     const CacheParams P = params(a);
     const bool wide = wide_rows(a);
-    if (a.dtype == LI_DTYPE_BF16) read_type<__nv_bfloat16>(P, wide, blocks_of(P), st);
-    else if (a.dtype == LI_DTYPE_FP16) read_type<__half>(P, wide, blocks_of(P), st);
-    else read_type<float>(P, wide, blocks_of(P), st);
+    if (a.dtype == LI_DTYPE_BF16) read_type<__nv_bfloat16>(P, wide, st);
+    else if (a.dtype == LI_DTYPE_FP16) read_type<__half>(P, wide, st);
+    else read_type<float>(P, wide, st);
     return cudaGetLastError();
 }
 
