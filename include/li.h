@@ -569,8 +569,8 @@ li_status li_cache_read(const li_cache_args *args, void *stream);
  * significant bits), the codes as they are, sums in fp32; the scores are exact to fp32 rounding,
  * the weights to 2^-9 relative, the normaliser sums the unrounded weights.
  * The workspace (li_cache_attention_workspace_size bytes, 256-byte aligned; it depends on the
- * current device's SM count) holds partial outputs when a few rows are cut between SMs; contents on
- * entry are ignored, and calls that may overlap need their own. Stream-ordered, no allocation,
+ * current device's SM count, and may be NULL where that is 0) holds partial outputs when a few rows
+ * are cut between SMs; contents on entry are ignored, and calls that may overlap need their own. Stream-ordered, no allocation,
  * graph-capturable, deterministic (bit-identical reruns on one device model).
  */
 typedef struct li_cache_attn_args {

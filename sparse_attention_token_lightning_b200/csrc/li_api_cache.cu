@@ -198,7 +198,7 @@ li_status validate_cache_attn(const li_cache_attn_args *a, li::CacheAttnPlan *p)
 }
 
 size_t cache_attn_bytes(const li::CacheAttnPlan &p) {
-    return li::align_up(p.partial_floats * sizeof(float) + 1, 256);
+    return li::align_up(p.partial_floats * sizeof(float), 256);
 }
 
 }  // namespace
@@ -295,9 +295,9 @@ li_status li_cache_attention(const li_cache_attn_args *args, void *workspace, si
     li::CacheAttnPlan p;
     li_status st = validate_cache_attn(args, &p);
     if (st != LI_OK) return st;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < cache_attn_bytes(p))
-        return fail(LI_ERR_WORKSPACE, "workspace must be a 256-byte aligned device buffer of >= %zu bytes",
-                    cache_attn_bytes(p));
+    const size_t need = cache_attn_bytes(p);
+    if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
+        return fail(LI_ERR_WORKSPACE, "workspace must be a 256-byte aligned device buffer of >= %zu bytes", need);
     if (p.units == 0) return ok();
     if (!out || !aligned(out, 16)) return fail(LI_ERR_INVALID_ARG, "out must be a 16-byte aligned device buffer");
     if ((softmax_max == nullptr) != (softmax_sum == nullptr) || !aligned(softmax_max, 4) || !aligned(softmax_sum, 4))

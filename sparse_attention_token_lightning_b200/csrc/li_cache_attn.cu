@@ -32,6 +32,8 @@
 //   scheduler the CTA's units;  qk / pv: one thread each issues the two products
 // Every wait is bounded in time; on expiry the kernel records LI_DEVERR_TIMEOUT and returns. The
 // softmax warps of a group agree on giving up (the vote carries it), so none is left at a barrier.
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -88,13 +90,12 @@ struct Bars {
     __device__ uint32_t s_empty(int i) const { return at(10 + i); }
     __device__ uint32_t p_full(int i) const { return at(12 + i); }
     __device__ uint32_t p_empty(int i) const { return at(14 + i); }
-    __device__ uint32_t o_done() const { return at(16); }
-    __device__ uint32_t o_empty() const { return at(17); }
-    __device__ uint32_t meta_full(int i) const { return at(18 + i); }
-    __device__ uint32_t slot_full(int i) const { return at(18 + kTileRing + i); }
-    __device__ uint32_t slot_empty(int i) const { return at(18 + kTileRing + kMaxSlots + i); }
+    __device__ uint32_t o_empty() const { return at(16); }
+    __device__ uint32_t meta_full(int i) const { return at(17 + i); }
+    __device__ uint32_t slot_full(int i) const { return at(17 + kTileRing + i); }
+    __device__ uint32_t slot_empty(int i) const { return at(17 + kTileRing + kMaxSlots + i); }
 };
-constexpr int kNumBars = 18 + kTileRing + 2 * kMaxSlots;
+constexpr int kNumBars = 17 + kTileRing + 2 * kMaxSlots;
 struct Tail {
     uint64_t bars[kNumBars];
     Unit unit[2];
@@ -574,10 +575,7 @@ __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
                     for (int k = 0; k < 4; ++k)
                         umma_f8(d, v + k * (32 * 128 >> 4), p + k * (32 * 2 * N >> 4), idesc, (j | k) != 0);
                     umma_commit(bars.slot_empty(sr.idx));
-                    if (c == P.blocks - 1) {
-                        umma_commit(bars.p_empty(kt & 1u));
-                        umma_commit(bars.o_done());
-                    }
+                    if (c == P.blocks - 1) umma_commit(bars.p_empty(kt & 1u));
                 }
                 __syncwarp();
             }
@@ -724,7 +722,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                     }
                 }
                 if (j > 0) {
-                    ok = ok && wait_warp(bars.o_done(), (kt - 1) & 1u, abort_flag);
+                    ok = ok && wait_warp(bars.p_empty(b ^ 1u), ((kt - 1) >> 1) & 1u, abort_flag);
                     tc_fence_after();
                     for (int c = 0; c < P.blocks; ++c) {
                         const uint32_t o = tmem + lanes + 2 * kSCols<N> + c * 2 * N + H * g;
@@ -744,6 +742,9 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                     tc_fence_before();
                 }
             }
+            // p_empty(i) completes with the value product of every second tile: it frees that tile's
+            // weights, and O holds all tiles up to it. A wait for tile t is sound because the wait
+            // below for tile t - 2 came before (a parity says nothing of phases further back)
             ok = ok && wait_warp(bars.p_empty(b), ((kt >> 1) & 1u) ^ 1u, abort_flag);
             // weights as hi + lo / 16, by way of fp16 (11 bits); a key's row of the operand
             uint32_t hi[H / 4], lo[H / 4];
@@ -785,7 +786,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 T->lsum[g][lane / (32 / H)][q] = ws;
                 if (kStats) T->mx[g][lane / (32 / H)][q] = wm;
             }
-            ok = ok && wait_warp(bars.o_done(), (kt - 1) & 1u, abort_flag);
+            ok = ok && wait_warp(bars.p_empty((kt - 1) & 1u), ((kt - 1) >> 1) & 1u, abort_flag);
             tc_fence_after();
             named_bar(bar_id, 128);
             ++nu;
@@ -909,7 +910,6 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(
             mbar_init(bars.p_full(i), 32 * R::kSoft);
             mbar_init(bars.p_empty(i), 1);
         }
-        mbar_init(bars.o_done(), 1);
         mbar_init(bars.o_empty(), R::kSoft);
         for (int i = 0; i < kTileRing; ++i) mbar_init(bars.meta_full(i), 32 * kGatherWarps);
         for (int i = 0; i < kMaxSlots; ++i) {
@@ -921,6 +921,8 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(
         if (P.has_rope) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_rope)) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    // the join may be launched now; it waits for this grid's end
+    if (P.split) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == R::kQk) {
         tmem_alloc(smem_u32(&T->tmem), P.tmem_cols);
         tmem_relinquish();
@@ -956,46 +958,61 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(
 // Joins the partial outputs of units that were cut between CTAs: with references r_i, sums l_i and
 // outputs o_i of the pieces, o = sum o_i 2^(r_i - r) / sum l_i 2^(r_i - r), r = max r_i. A unit
 // that lies in one CTA's share was written by it.
-constexpr int kJoinThreads = 128;
+// It is launched while the first kernel runs (programmatic dependent launch) and waits for its end.
+constexpr int kJoinThreads = 128, kMaxPieces = kMaxTopk / kKeys;
 __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __grid_constant__ Params P, int N, int grid) {
+    __shared__ float weight[kMaxPieces];                // 2^(r_i - r), 0 for a piece without keys
+    __shared__ float red[3][kJoinThreads / 32];
     const int64_t unit = blockIdx.x;
     const int64_t total = P.units * P.tiles;
     auto cta_of = [&](int64_t t) { return (int)(((t + 1) * grid + total - 1) / total - 1); };
-    const int c0 = cta_of(unit * P.tiles), c1 = cta_of((unit + 1) * P.tiles - 1);
-    if (c0 == c1) return;
+    const int c0 = cta_of(unit * P.tiles), pieces = cta_of((unit + 1) * P.tiles - 1) - c0 + 1;
     const int64_t row = unit / P.head_blocks;
     const int head0 = (int)(unit - row * P.head_blocks) * 32;
-    const int h = blockIdx.y;
-    if (head0 + h >= P.G || !idx_ok(row, P.rows, P.status)) return;
+    const int h = blockIdx.y, t = threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (pieces == 1 || head0 + h >= P.G || !idx_ok(row, P.rows, P.status)) return;
     const float kInf = __int_as_float(0x7f800000);
     // the unit's pieces: the first starts it (slot 1 of its CTA), the others continue (slot 0)
-    float r = kNoRef, m = -kInf;
-    for (int c = c0; c <= c1; ++c) {
-        const float *st = P.part_stat + ((int64_t)(2 * c + (c == c0)) * N + h) * 3;
-        r = fmaxf(r, st[0]);
-        m = fmaxf(m, st[2]);
+    const auto slot = [&](int i) { return (int64_t)(2 * (c0 + i) + (i == 0)) * N + h; };
+    float r = kNoRef, l = 0.0f, m = -kInf;
+    if (t < pieces) {
+        const float *st = P.part_stat + slot(t) * 3;
+        r = st[0];
+        l = st[1];
+        m = st[2];
     }
-    float l = 0.0f;
-    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c = c0; c <= c1; ++c) {
-        const int64_t slot = (int64_t)(2 * c + (c == c0)) * N + h;
-        const float *st = P.part_stat + slot * 3;
-        if (st[1] == 0.0f) continue;                    // no key of this piece counts
-        const float w = exp2_(st[0] - r);
-        l = fmaf(st[1], w, l);
+    const float wr = warp_max(r), wm = warp_max(m);
+    if ((t & 31) == 0) {
+        red[0][t >> 5] = wr;
+        red[1][t >> 5] = wm;
+    }
+    __syncthreads();
+    const float most = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    m = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
+    const float w = l == 0.0f ? 0.0f : exp2_(r - most);
+    if (t < pieces) weight[t] = w;
+    l *= w;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < P.blocks) o[i] = fmaf(P.part_o[slot * P.Dm + 128 * i + threadIdx.x], w, o[i]);
-    }
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if ((t & 31) == 0) red[2][t >> 5] = l;
+    __syncthreads();
+    l = (red[2][0] + red[2][1]) + (red[2][2] + red[2][3]);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int64_t at = row * P.G + head0 + h;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < P.blocks)
-            P.out[at * P.Dm + 128 * i + threadIdx.x] = __bfloat16_as_ushort(__float2bfloat16_rn(o[i] * inv));
-    if (threadIdx.x == 0 && P.smax) {
+    for (int c = 0; c < P.blocks; ++c) {
+        float o = 0.0f;
+#pragma unroll 8
+        for (int i = 0; i < pieces; ++i) {
+            const float f = weight[i];
+            // what a piece without keys left is never written: not even a NaN of it may count
+            if (f != 0.0f) o = fmaf(P.part_o[slot(i) * P.Dm + 128 * c + t], f, o);
+        }
+        P.out[at * P.Dm + 128 * c + t] = __bfloat16_as_ushort(__float2bfloat16_rn(o * inv));
+    }
+    if (t == 0 && P.smax) {
         P.smax[at] = m > -kInf ? m * kLn2 : m;
-        P.ssum[at] = m > -kInf ? l * exp2_(r - m) : l;
+        P.ssum[at] = m > -kInf ? l * exp2_(most - m) : l;
     }
 }
 
@@ -1010,6 +1027,27 @@ bool make_row_map(CUtensorMap *m, const void *ptr, CUtensorMapDataType type, int
     return fn(m, type, 2, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Lets a kernel use kSmemBytes of shared memory, once per kernel and device.
+template <auto kKernel> cudaError_t allow_smem() {
+    static std::atomic<uint64_t> done{0};               // bit per device below 64
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1u)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+    return e;
+}
+
+template <int N, bool kStats>
+cudaError_t launch_main(const CUtensorMap &tm_codes, const CUtensorMap &tm_rope, const Params &P, int grid,
+                        cudaStream_t st) {
+    cudaError_t e = allow_smem<cache_attn_kernel<N, kStats>>();
+    if (e != cudaSuccess) return e;
+    cache_attn_kernel<N, kStats><<<grid, Roles<N>::kThreads, kSmemBytes, st>>>(tm_codes, tm_rope, P);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -1106,19 +1144,22 @@ cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnP
     } else {
         tm_rope = tm_codes;
     }
-    auto run = [&](auto kern, int threads) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-        if (e != cudaSuccess) return e;
-        kern<<<p.grid, threads, kSmemBytes, st>>>(tm_codes, tm_rope, P);
-        return cudaGetLastError();
-    };
     // the statistics cost a maximum per score: a kernel of their own
-    cudaError_t e = p.N == 16 ? run(smax ? cache_attn_kernel<16, true> : cache_attn_kernel<16, false>, Roles<16>::kThreads)
-                              : run(smax ? cache_attn_kernel<32, true> : cache_attn_kernel<32, false>, Roles<32>::kThreads);
+    cudaError_t e = p.N == 16 ? (smax ? launch_main<16, true>(tm_codes, tm_rope, P, p.grid, st)
+                                      : launch_main<16, false>(tm_codes, tm_rope, P, p.grid, st))
+                              : (smax ? launch_main<32, true>(tm_codes, tm_rope, P, p.grid, st)
+                                      : launch_main<32, false>(tm_codes, tm_rope, P, p.grid, st));
     if (e != cudaSuccess || !p.split) return e;
-    const dim3 grid((unsigned)p.units, (unsigned)(a.G < 32 ? a.G : 32));
-    cache_attn_join_kernel<<<grid, kJoinThreads, 0, st>>>(P, p.N, p.grid);
-    return cudaGetLastError();
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)p.units, (unsigned)(a.G < 32 ? a.G : 32));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel, P, p.N, p.grid);
 }
 
 }  // namespace li

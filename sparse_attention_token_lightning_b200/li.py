@@ -11,7 +11,6 @@ There is no fallback: if the library is missing, loading raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from pathlib import Path
 
@@ -499,27 +498,38 @@ def sparse_attention(ap, stream=None, check: bool = True):
 
 # ---- rotary positions and the quantised key cache ------------------------------------------------
 
-_HERE = contextlib.nullcontext()
+# Decode calls these once a layer, so the binding's own time counts: a call of a few microseconds
+# on the device spends about as long here. The helpers check with plain attribute reads.
+_FLOATS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # li_dtype of unquantised data
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _using(dev):
-    """A context in which `dev` is the current device."""
-    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+def _device_of(t, name):
+    """The CUDA device of a call's first tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
+    return t.device
 
 
 def _raw_stream(dev, stream):
     """Handle of `stream`, or of the device's current stream."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index) or None
+        return _current_raw_stream(dev.index)
     if stream.device != dev:
         raise ValueError(f"a stream of {stream.device} with tensors on {dev}")
-    return stream.cuda_stream or None
+    return stream.cuda_stream
 
 
-def _on_device(call, args, dev, stream):
-    """call(args, stream) with `dev` current: on `stream`, or on the device's current stream."""
-    with _using(dev):
-        _check(call(ctypes.byref(args), _raw_stream(dev, stream)))
+def _on_device(dev, call, *args):
+    """call(*args) with `dev` current, its status checked."""
+    if dev.index == _current_device():
+        st = call(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = call(*args)
+    if st:
+        raise LiError(st, li_last_error_string())
 
 
 def _empty(like, shape, dtype, stream):
@@ -530,32 +540,43 @@ def _empty(like, shape, dtype, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _cuda(t, dev, name, dtype=None, shape=None):
-    """`t` is a CUDA tensor on `dev`, of the given type and shape where they are given."""
-    if t.device != dev or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {dev}, got one on {t.device}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _empty_like(t, stream):
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
 
 
-def _contiguous(t, dev, name, dtype=None, shape=None):
-    _cuda(t, dev, name, dtype, shape)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _on(t, dev, name):
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got a tensor on {t.device}")
+
+
+def _ptr_of(t, dev, name, dtype, shape):
+    """Address of a contiguous tensor on `dev` of the given type and shape."""
+    if t.device != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
     return t.data_ptr()
 
 
-def _row_stride(t, lead, name):
+def _status_ptr(t, dev):
+    if t.device != dev or t.element_size() != 4 or t.numel() < 1:
+        raise ValueError(f"device_status must be a 4-byte tensor on {dev}")
+    return t.data_ptr()
+
+
+def _row_stride(shape, strides, lead, name):
     """(rows, stride) of the first `lead` dimensions taken as one, e.g. (B, S) of (B, S, N, D)."""
-    shape, strides = t.shape, t.stride()
+    if lead == 1:
+        return shape[0], strides[0]
     rows, step = 1, 0
-    for n, s in zip(reversed(shape[:lead]), reversed(strides[:lead])):
+    for i in range(lead - 1, -1, -1):
+        n = shape[i]
         if n != 1:
             if rows == 1:
-                step = s
-            elif s != rows * step and rows:
+                step = strides[i]
+            elif rows and strides[i] != rows * step:
                 raise ValueError(f"the leading dimensions of {name} must flatten to one stride")
             rows *= n
     return rows, step
@@ -589,31 +610,28 @@ def rope_frequencies(rope_dim: int, base: float = 10000.0, scaling: str | None =
 
 
 def _rope(call, x, positions, freqs, offset, interleaved, out, stream):
-    if x.dim() < 2:
-        raise ValueError("x must be (..., heads, head_dim)")
-    dev, lead = x.device, x.dim() - 2
-    _cuda(x, dev, "x")
-    if x.dtype not in DTYPES or x.dtype == torch.float8_e4m3fn:
-        raise ValueError(f"x must be bf16, fp16 or fp32, got {x.dtype}")
-    if x.shape[-1] > 1 and x.stride(-1) != 1:
-        raise ValueError("the last dimension of x must be dense")
-    if positions.dtype not in (torch.int32, torch.int64):
-        raise ValueError(f"positions must be int32 or int64, got {positions.dtype}")
-    pos = _contiguous(positions, dev, "positions", shape=x.shape[:lead])
-    rows, x_row = _row_stride(x, lead, "x")
+    dev, shape, strides, dtype = _device_of(x, "x"), x.shape, x.stride(), _FLOATS.get(x.dtype)
+    lead = len(shape) - 2
+    if lead < 0 or dtype is None:
+        raise ValueError(f"x must be (..., heads, head_dim), bf16, fp16 or fp32, got {x.dtype} {tuple(shape)}")
+    pos_type = positions.dtype
+    if pos_type is not torch.int64 and pos_type is not torch.int32:
+        raise ValueError(f"positions must be int32 or int64, got {pos_type}")
+    pos = _ptr_of(positions, dev, "positions", pos_type, shape[:lead])
+    rows, x_row = _row_stride(shape, strides, lead, "x")
     if out is None:
-        out = _empty(x, x.shape, x.dtype, stream)
-    elif out is not x:
-        _cuda(out, dev, "out", x.dtype, x.shape)
-        if out.shape[-1] > 1 and out.stride(-1) != 1:
-            raise ValueError("the last dimension of out must be dense")
-    _, y_row = _row_stride(out, lead, "out")
-    heads, dim = x.shape[-2:]
-    a = LiRopeArgs(x.data_ptr(), out.data_ptr(), pos, rows, x_row, x.stride(-2), y_row,
-                   out.stride(-2), heads, dim, freqs.rope_dim, offset, int(bool(interleaved)),
-                   DTYPES[x.dtype], 64 if positions.dtype == torch.int64 else 32,
-                   freqs.magnitude, freqs.freq)
-    _on_device(call, a, dev, stream)
+        out = _empty_like(x, stream)
+    elif out is not x and (out.device != dev or out.dtype is not x.dtype or out.shape != shape):
+        raise ValueError(f"out must be {x.dtype} {tuple(shape)} on {dev}, got {out.dtype} "
+                         f"{tuple(out.shape)} on {out.device}")
+    to = out.stride()
+    if shape[-1] > 1 and (strides[-1] != 1 or to[-1] != 1):
+        raise ValueError("the last dimension of x and out must be dense")
+    a = LiRopeArgs(x.data_ptr(), out.data_ptr(), pos, rows, x_row, strides[-2],
+                   _row_stride(shape, to, lead, "out")[1], to[-2], shape[-2], shape[-1],
+                   freqs.rope_dim, offset, 1 if interleaved else 0, dtype,
+                   64 if pos_type is torch.int64 else 32, freqs.magnitude, freqs.freq)
+    _on_device(dev, call, ctypes.byref(a), _raw_stream(dev, stream))
     return out
 
 
@@ -634,104 +652,96 @@ def rope_grad(dy, positions, freqs: RopeFrequencies, offset: int = 0, interleave
 
 def _no_head(t, dims, name):
     """(..., 1, D) seen as (..., D): keys have one head."""
-    if t.dim() == dims + 1 and t.shape[-2] == 1:
-        return t.squeeze(-2)
-    if t.dim() != dims:
-        raise ValueError(f"{name} has {t.dim()} dimensions, {dims} (or one head more) wanted")
-    return t
-
-
-def _rows_arg(t, dims, name):
-    """Batch and row stride of rows (B, S, D) or (T, D)."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"the last dimension of {name} must be dense")
-    st = t.stride()
-    return (st[0] if dims == 3 else 0), st[-2]
+    n = t.dim()
+    if n == dims:
+        return t
+    if n != dims + 1 or t.shape[-2] != 1:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, {dims} dimensions (or a head of 1 more) wanted")
+    return t.squeeze(-2)
 
 
 def make_cache_args(x, codes, descale, rope=None, rope_cache=None, seqused_k=None,
                     block_table=None, cu_seqlens=None, seqused=None, pow2=False,
                     device_status=None) -> LiCacheArgs:
     """li_cache_args of device tensors (see cache_write)."""
-    dev = x.device
-    _cuda(x, dev, "x")
-    if x.dtype not in DTYPES or x.dtype == torch.float8_e4m3fn:
-        raise ValueError(f"x must be bf16, fp16 or fp32, got {x.dtype}")
-    if (rope is None) != (rope_cache is None):
-        raise ValueError("rope and rope_cache go together")
+    dev, kind = _device_of(x, "x"), x.dtype
+    dtype = _FLOATS.get(kind)
+    if dtype is None:
+        raise ValueError(f"x must be bf16, fp16 or fp32, got {kind}")
+    a = LiCacheArgs()
     tnd = cu_seqlens is not None
     dims = 2 if tnd else 3
-    x = _no_head(x, dims, "x")
-    D = x.shape[-1]
-    a = LiCacheArgs()
-    a.x = x.data_ptr()
-    a.x_batch_stride, a.x_row_stride = _rows_arg(x, dims, "x")
-    rows = x.shape[:-1]
+    x, codes = _no_head(x, dims, "x"), _no_head(codes, 3, "codes")
+    shape, strides = x.shape, x.stride()
+    D, (n0, n1, _) = shape[-1], codes.shape
+    if D > 1 and strides[-1] != 1:
+        raise ValueError("the last dimension of x must be dense")
+    a.x, a.x_row_stride = x.data_ptr(), strides[-2]
     if tnd:
-        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
-            raise ValueError("cu_seqlens must have shape (B + 1,)")
-        a.cu_seqlens = _contiguous(cu_seqlens, dev, "cu_seqlens", torch.int32)
         B = cu_seqlens.shape[0] - 1
-        a.layout_x, a.x_len = LAYOUTS["TND"], rows[0]
+        a.cu_seqlens = _ptr_of(cu_seqlens, dev, "cu_seqlens", torch.int32, (max(B, 0) + 1,))
+        a.layout_x, a.x_len = 1, shape[0]
     else:
-        B = rows[0]
-        a.layout_x, a.x_len = LAYOUTS["BSND"], rows[1]
-    a.batch = B
-    codes = _no_head(codes, 3, "codes")
-    grid = codes.shape[:2]
-    a.codes = _contiguous(codes, dev, "codes", torch.float8_e4m3fn, (*grid, D))
-    a.descale = _contiguous(descale, dev, "descale", torch.float32, grid)
-    a.dim, a.dtype, a.pow2 = D, DTYPES[x.dtype], int(bool(pow2))
+        B = shape[0]
+        a.x_len, a.x_batch_stride = shape[1], strides[0]
+    a.batch, a.dim, a.dtype = B, D, dtype
+    a.codes = _ptr_of(codes, dev, "codes", torch.float8_e4m3fn, (n0, n1, D))
+    a.descale = _ptr_of(descale, dev, "descale", torch.float32, (n0, n1))
+    if pow2:
+        a.pow2 = 1
     if block_table is not None:
-        a.layout_k = LAYOUTS["PA_BSND"]
-        a.num_blocks, a.block_size = grid
-        if block_table.dim() != 2 or block_table.shape[0] != B:
-            raise ValueError(f"block_table must be ({B}, blocks), got {tuple(block_table.shape)}")
-        a.block_table = _contiguous(block_table, dev, "block_table", torch.int32)
-        a.block_table_stride = block_table.shape[1]
+        a.layout_k, a.num_blocks, a.block_size = 2, n0, n1
+        width = block_table.shape[-1]
+        a.block_table = _ptr_of(block_table, dev, "block_table", torch.int32, (B, width))
+        a.block_table_stride = width
     else:
-        if grid[0] != B:
-            raise ValueError(f"a dense cache of {grid[0]} batches, {B} wanted")
-        a.layout_k, a.k_len = LAYOUTS["BSND"], grid[1]
+        if n0 != B:
+            raise ValueError(f"a dense cache of {n0} batches, {B} wanted")
+        a.k_len = n1
     if seqused is not None:
-        a.seqused = _contiguous(seqused, dev, "seqused", torch.int32, (B,))
+        a.seqused = _ptr_of(seqused, dev, "seqused", torch.int32, (B,))
     if seqused_k is not None:
-        a.seqused_k = _contiguous(seqused_k, dev, "seqused_k", torch.int32, (B,))
+        a.seqused_k = _ptr_of(seqused_k, dev, "seqused_k", torch.int32, (B,))
+    if (rope is None) != (rope_cache is None):
+        raise ValueError("rope and rope_cache go together")
     if rope is not None:
         rope = _no_head(rope, dims, "rope")
-        R = rope.shape[-1]
-        _cuda(rope, dev, "rope", x.dtype, (*rows, R))
-        a.rope = rope.data_ptr()
-        a.rope_batch_stride, a.rope_row_stride = _rows_arg(rope, dims, "rope")
-        a.rope_cache = _contiguous(_no_head(rope_cache, 3, "rope_cache"), dev, "rope_cache",
-                                   x.dtype, (*grid, R))
-        a.rope_dim = R
+        R, strides = rope.shape[-1], rope.stride()
+        if rope.device != dev or rope.dtype is not kind or rope.shape[:-1] != shape[:-1] or (R > 1 and strides[-1] != 1):
+            raise ValueError(f"rope must be {kind} {tuple(shape[:-1])} + (rope_dim,) on {dev}, its last "
+                             f"dimension dense, got {rope.dtype} {tuple(rope.shape)} on {rope.device}")
+        a.rope, a.rope_row_stride, a.rope_dim = rope.data_ptr(), strides[-2], R
+        if not tnd:
+            a.rope_batch_stride = strides[0]
+        a.rope_cache = _ptr_of(_no_head(rope_cache, 3, "rope_cache"), dev, "rope_cache", kind, (n0, n1, R))
     if device_status is not None:
-        if device_status.element_size() != 4:
-            raise ValueError("device_status must be a 4-byte tensor")
-        a.device_status = _contiguous(device_status, dev, "device_status")
+        a.device_status = _status_ptr(device_status, dev)
     return a
 
 
 def _checked(call, a, dev, stream, device_status, check):
     """Runs a call whose args have a device_status; with check, raises on its bits."""
-    own = check and device_status is None
-    if own:
-        device_status = _empty_status(dev, stream)
+    if check and device_status is None:
+        device_status = _zero_status(dev, stream)
         a.device_status = device_status.data_ptr()
-    _on_device(call, a, dev, stream)
+    _on_device(dev, call, ctypes.byref(a), _raw_stream(dev, stream))
     if check:
-        with torch.cuda.device(dev):
-            st, bits = li_check_status(device_status, stream)
-        if st != LI_OK:
-            raise LiError(st, f"{li_last_error_string()} (device bits 0x{bits:x})")
+        _raise_on(dev, device_status, stream)
 
 
-def _empty_status(dev, stream):
+def _zero_status(dev, stream):
     if stream is None:
         return torch.zeros(1, dtype=torch.int32, device=dev)
     with torch.cuda.stream(stream):
         return torch.zeros(1, dtype=torch.int32, device=dev)
+
+
+def _raise_on(dev, device_status, stream):
+    """Waits for the call and raises LiError if it set a status bit."""
+    with torch.cuda.device(dev):
+        st, bits = li_check_status(device_status, stream)
+    if st != LI_OK:
+        raise LiError(st, f"{li_last_error_string()} (device bits 0x{bits:x})")
 
 
 def cache_write(x, codes, descale, rope=None, rope_cache=None, seqused_k=None, block_table=None,
@@ -768,43 +778,37 @@ def cache_read(codes, descale, out, rope_cache=None, rope_out=None, seqused_k=No
 def make_cache_attn_args(q, codes, descale, sparse_indices, scale, q_rope=None, rope_cache=None,
                          block_table=None, s2=None, device_status=None) -> LiCacheAttnArgs:
     """li_cache_attn_args of device tensors (see cache_attention)."""
-    dev = q.device
+    dev = _device_of(q, "q")
     if q.dim() != 4:
         raise ValueError("q must be (B, S1, G, Dm)")
-    B, S1, G, Dm = q.shape
+    B, S1, G, Dm = shape = q.shape
     a = LiCacheAttnArgs()
-    a.q = _contiguous(q, dev, "q", torch.bfloat16)
+    a.q = _ptr_of(q, dev, "q", torch.bfloat16, shape)
     codes = _no_head(codes, 3, "codes")
-    grid = codes.shape[:2]
-    a.codes = _contiguous(codes, dev, "codes", torch.float8_e4m3fn, (*grid, Dm))
-    a.descale = _contiguous(descale, dev, "descale", torch.float32, grid)
+    n0, n1, _ = codes.shape
+    a.codes = _ptr_of(codes, dev, "codes", torch.float8_e4m3fn, (n0, n1, Dm))
+    a.descale = _ptr_of(descale, dev, "descale", torch.float32, (n0, n1))
     topk = sparse_indices.shape[-1]
-    a.sparse_indices = _contiguous(sparse_indices, dev, "sparse_indices", torch.int32, (B, S1, 1, topk))
-    a.scale, a.batch, a.s1, a.G, a.Dm, a.topk = float(scale), B, S1, G, Dm, topk
+    a.sparse_indices = _ptr_of(sparse_indices, dev, "sparse_indices", torch.int32, (B, S1, 1, topk))
+    a.scale, a.batch, a.s1, a.G, a.Dm, a.topk = scale, B, S1, G, Dm, topk
     if (q_rope is None) != (rope_cache is None):
         raise ValueError("q_rope and rope_cache go together")
     if q_rope is not None:
         R = q_rope.shape[-1]
-        a.q_rope = _contiguous(q_rope, dev, "q_rope", torch.bfloat16, (B, S1, G, R))
-        a.k_rope = _contiguous(_no_head(rope_cache, 3, "rope_cache"), dev, "rope_cache",
-                               torch.bfloat16, (*grid, R))
+        a.q_rope = _ptr_of(q_rope, dev, "q_rope", torch.bfloat16, (B, S1, G, R))
+        a.k_rope = _ptr_of(_no_head(rope_cache, 3, "rope_cache"), dev, "rope_cache", torch.bfloat16, (n0, n1, R))
         a.Dr = R
     if block_table is not None:
-        if block_table.dim() != 2 or block_table.shape[0] != B:
-            raise ValueError(f"block_table must be ({B}, blocks), got {tuple(block_table.shape)}")
-        a.layout_k = LAYOUTS["PA_BSND"]
-        a.block_table = _contiguous(block_table, dev, "block_table", torch.int32)
-        a.block_table_stride = block_table.shape[1]
-        a.num_blocks, a.block_size = grid
-        a.s2 = block_table.shape[1] * grid[1] if s2 is None else s2
+        width = block_table.shape[-1]
+        a.block_table = _ptr_of(block_table, dev, "block_table", torch.int32, (B, width))
+        a.block_table_stride, a.layout_k, a.num_blocks, a.block_size = width, 2, n0, n1
+        a.s2 = width * n1 if s2 is None else s2
     else:
-        if grid[0] != B or (s2 is not None and s2 != grid[1]):
-            raise ValueError(f"a dense cache of shape {tuple(grid)} with B={B}, s2={s2}")
-        a.s2 = grid[1]
+        if n0 != B or (s2 is not None and s2 != n1):
+            raise ValueError(f"a dense cache of shape {(n0, n1)} with B={B}, s2={s2}")
+        a.s2 = n1
     if device_status is not None:
-        if device_status.element_size() != 4:
-            raise ValueError("device_status must be a 4-byte tensor")
-        a.device_status = _contiguous(device_status, dev, "device_status")
+        a.device_status = _status_ptr(device_status, dev)
     return a
 
 
@@ -818,27 +822,22 @@ def cache_attention(q, codes, descale, sparse_indices, scale, q_rope=None, rope_
     G, Dm) bf16, or (out, softmax_max, softmax_sum) with return_stats, (B, 1, S1, G) fp32."""
     a = make_cache_attn_args(q, codes, descale, sparse_indices, scale, q_rope, rope_cache,
                              block_table, s2, device_status)
-    dev = q.device
-    L = lib()
-    n = ctypes.c_size_t(0)
-    own = check and device_status is None
-    if own:
-        device_status = _empty_status(dev, stream)
+    dev, L, n = q.device, lib(), ctypes.c_size_t(0)
+    if check and device_status is None:
+        device_status = _zero_status(dev, stream)
         a.device_status = device_status.data_ptr()
-    with _using(dev):
-        _check(L.li_cache_attention_workspace_size(ctypes.byref(a), ctypes.byref(n)))
-        ws = _empty(q, n.value, torch.uint8, stream)
-        out = _empty(q, q.shape, torch.bfloat16, stream)
-        smax = ssum = None
-        if return_stats:
-            shape = (q.shape[0], 1, q.shape[1], q.shape[2])
-            smax, ssum = (_empty(q, shape, torch.float32, stream) for _ in range(2))
-        _check(L.li_cache_attention(ctypes.byref(a), ws.data_ptr(), n.value, out.data_ptr(), _ptr(smax),
-                                    _ptr(ssum), _raw_stream(dev, stream)))
-        if check:
-            st, bits = li_check_status(device_status, stream)
-            if st != LI_OK:
-                raise LiError(st, f"{li_last_error_string()} (device bits 0x{bits:x})")
+    ref = ctypes.byref(a)
+    _on_device(dev, L.li_cache_attention_workspace_size, ref, ctypes.byref(n))
+    ws = _empty(q, n.value, torch.uint8, stream) if n.value else None      # alive until the launch
+    out = _empty_like(q, stream)
+    smax = ssum = None
+    if return_stats:
+        shape = (q.shape[0], 1, q.shape[1], q.shape[2])
+        smax, ssum = (_empty(q, shape, torch.float32, stream) for _ in range(2))
+    _on_device(dev, L.li_cache_attention, ref, _ptr(ws), n.value, out.data_ptr(), _ptr(smax), _ptr(ssum),
+               _raw_stream(dev, stream))
+    if check:
+        _raise_on(dev, device_status, stream)
     return (out, smax, ssum) if return_stats else out
 
 

@@ -1,5 +1,9 @@
 """Attention over the E4M3 cache (li_cache_attention) against a 64-bit form; tolerances are derived
 in cache_attn_ref from the kernel's arithmetic."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -190,6 +194,31 @@ def test_reruns_graphs_and_streams_are_bit_identical():
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(a, o)
+
+
+FIRST_CALL = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+import cache_attn_ref as ref
+from sparse_attention_token_lightning_b200 import li
+p = ref.make(1, 200, 200, 16, 512, 64, 150, causal=True, seed=6)
+c = lambda t: t.cuda()
+args = c(p.q), c(p.codes), c(p.descale), c(p.idx), p.scale
+kw = dict(q_rope=c(p.q_rope), rope_cache=c(p.k_rope), block_table=c(p.table), s2=p.s2, check=False)
+outs = [li.cache_attention(*args, **kw) for _ in range(4)]
+torch.cuda.synchronize()
+ref.check(p, outs[0], rows=range(0, 200, 3))
+assert all(torch.equal(outs[0], o) for o in outs[1:])
+"""
+
+
+def test_the_first_call_of_a_process():
+    """A cold start spreads the kernel's roles in time as no later call does: its bits are those of
+    every other call."""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALL.format(root=os.path.dirname(tests), tests=tests)
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
 
 
 def test_no_rows():
