@@ -959,60 +959,68 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(
 // outputs o_i of the pieces, o = sum o_i 2^(r_i - r) / sum l_i 2^(r_i - r), r = max r_i. A unit
 // that lies in one CTA's share was written by it.
 // It is launched while the first kernel runs (programmatic dependent launch) and waits for its end.
-constexpr int kJoinThreads = 128, kMaxPieces = kMaxTopk / kKeys;
+// A block joins one head: four dims a thread, every warp with the weights of its own, all pieces'
+// reads in flight.
+constexpr int kJoinThreads = 128;
+static_assert(kMaxTopk / kKeys <= 64, "two pieces a lane");
 __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __grid_constant__ Params P, int N, int grid) {
-    __shared__ float weight[kMaxPieces];                // 2^(r_i - r), 0 for a piece without keys
-    __shared__ float red[3][kJoinThreads / 32];
-    const int64_t unit = blockIdx.x;
-    const int64_t total = P.units * P.tiles;
-    auto cta_of = [&](int64_t t) { return (int)(((t + 1) * grid + total - 1) / total - 1); };
+    // rows are cut only where units x tiles x grid is far inside 32 bits
+    const uint32_t unit = blockIdx.x, total = (uint32_t)(P.units * P.tiles);
+    auto cta_of = [&](uint32_t t) { return (int)(((t + 1) * grid + total - 1) / total - 1); };
     const int c0 = cta_of(unit * P.tiles), pieces = cta_of((unit + 1) * P.tiles - 1) - c0 + 1;
-    const int64_t row = unit / P.head_blocks;
-    const int head0 = (int)(unit - row * P.head_blocks) * 32;
-    const int h = blockIdx.y, t = threadIdx.x;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int32_t row = unit / P.head_blocks, head0 = (int)(unit - row * P.head_blocks) * 32;
+    const int h = blockIdx.y, t = threadIdx.x, lane = t & 31;
     if (pieces == 1 || head0 + h >= P.G || !idx_ok(row, P.rows, P.status)) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const float kInf = __int_as_float(0x7f800000);
     // the unit's pieces: the first starts it (slot 1 of its CTA), the others continue (slot 0)
     const auto slot = [&](int i) { return (int64_t)(2 * (c0 + i) + (i == 0)) * N + h; };
-    float r = kNoRef, l = 0.0f, m = -kInf;
-    if (t < pieces) {
-        const float *st = P.part_stat + slot(t) * 3;
-        r = st[0];
-        l = st[1];
-        m = st[2];
-    }
-    const float wr = warp_max(r), wm = warp_max(m);
-    if ((t & 31) == 0) {
-        red[0][t >> 5] = wr;
-        red[1][t >> 5] = wm;
-    }
-    __syncthreads();
-    const float most = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    m = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
-    const float w = l == 0.0f ? 0.0f : exp2_(r - most);
-    if (t < pieces) weight[t] = w;
-    l *= w;
+    float r[2], l[2], w[2], most = kNoRef, m = -kInf, sum = 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if ((t & 31) == 0) red[2][t >> 5] = l;
-    __syncthreads();
-    l = (red[2][0] + red[2][1]) + (red[2][2] + red[2][3]);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int64_t at = row * P.G + head0 + h;
-    for (int c = 0; c < P.blocks; ++c) {
-        float o = 0.0f;
-#pragma unroll 8
-        for (int i = 0; i < pieces; ++i) {
-            const float f = weight[i];
-            // what a piece without keys left is never written: not even a NaN of it may count
-            if (f != 0.0f) o = fmaf(P.part_o[slot(i) * P.Dm + 128 * c + t], f, o);
+    for (int k = 0; k < 2; ++k) {
+        r[k] = kNoRef;
+        l[k] = 0.0f;
+        if (lane + 32 * k < pieces) {
+            const float *st = P.part_stat + slot(lane + 32 * k) * 3;
+            r[k] = st[0];
+            l[k] = st[1];
+            m = fmaxf(m, st[2]);
         }
-        P.out[at * P.Dm + 128 * c + t] = __bfloat16_as_ushort(__float2bfloat16_rn(o * inv));
+        most = fmaxf(most, r[k]);
+    }
+    most = warp_max(most);
+    m = warp_max(m);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        w[k] = l[k] == 0.0f ? 0.0f : exp2_(r[k] - most);    // 0: a piece without keys
+        sum = fmaf(l[k], w[k], sum);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int64_t at = (int64_t)row * P.G + head0 + h;
+    const bool mine = 4 * t < P.Dm;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) {
+        const float f = __shfl_sync(0xffffffffu, i < 32 ? w[0] : w[1], i & 31);
+        // a piece without keys left nothing here: not even a NaN of what lies there may count
+        if (mine && f != 0.0f) {
+            const float4 v = *reinterpret_cast<const float4 *>(P.part_o + slot(i) * P.Dm + 4 * t);
+            o.x = fmaf(v.x, f, o.x);
+            o.y = fmaf(v.y, f, o.y);
+            o.z = fmaf(v.z, f, o.z);
+            o.w = fmaf(v.w, f, o.w);
+        }
+    }
+    if (mine) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2 *>(P.out + at * P.Dm + 4 * t) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
     }
     if (t == 0 && P.smax) {
         P.smax[at] = m > -kInf ? m * kLn2 : m;
-        P.ssum[at] = m > -kInf ? l * exp2_(most - m) : l;
+        P.ssum[at] = m > -kInf ? sum * exp2_(most - m) : sum;
     }
 }
 
