@@ -39,6 +39,7 @@
 #include <cuda_fp8.h>
 
 #include "li_cache_attn.cuh"
+#include "li_fixed_div.cuh"
 #include "li_internal.cuh"
 #include "li_sm100.cuh"
 
@@ -58,6 +59,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // A tile's largest weight is set to 2^kShift when the reference moves, and it moves when a weight
 // would pass 2^kTop (of the 448 that E4M3 holds).
 constexpr float kShift = 4.0f, kTop = 8.0f;
+constexpr uint32_t kNoKey = 0xffc0ffeeu;            // a NaN that marks it
 constexpr float kNoRef = -1e30f;                    // reference of a piece without keys
 constexpr float kMinDescale = 7.888609052210118e-31f, kMaxDescale = 1.2676506002282294e30f;  // 2^+-100
 constexpr uint32_t kDevErrInternal = 0x20u;
@@ -71,6 +73,8 @@ template <int N> struct Roles {
     static constexpr int kThreads = 32 * (kSched + 3);
 };
 
+// What a CTA works on in turn. Every role finds its units by itself (unit_at); only the tiles that
+// are left once those behind the last selected entry are dropped come from the scheduler.
 struct Unit {
     int32_t row;            // -1: no more units
     int32_t head0;          // first head
@@ -98,7 +102,7 @@ struct Bars {
 constexpr int kNumBars = 17 + kTileRing + 2 * kMaxSlots;
 struct Tail {
     uint64_t bars[kNumBars];
-    Unit unit[2];
+    int32_t tiles[2];                           // the units' tiles left
     uint32_t tmem;
     volatile int abort_flag;
     alignas(16) int vote[2][2][4];              // [group][tile parity][warp]
@@ -108,7 +112,7 @@ struct Tail {
     int seen[2][16], fresh[2];                  // whether a head's reference is set; any that is not
     alignas(16) float red[2][16][4];            // [group][head][warp]
     alignas(16) float lsum[2][16][4], mx[2][16][4];
-    alignas(16) float descale[kTileRing][kKeys];    // 0: the entry selects nothing
+    alignas(16) float descale[kTileRing][kKeys];    // kNoKey: the entry selects nothing
 };
 static_assert(sizeof(Tail) <= kTailBytes, "shared memory tail");
 
@@ -129,6 +133,7 @@ struct Params {
     int32_t has_rope, blocks, head_blocks, tiles, split;
     int32_t q_bufs, slots;
     uint32_t q_bytes, p_off, slot_off, tmem_cols;
+    FixedDiv by_block, by_s1;
 };
 
 struct Ring {
@@ -253,60 +258,72 @@ __device__ __forceinline__ float transpose_reduce(const float (&v)[H], int lane)
     return a[0];
 }
 
-// First tile of CTA c's share of all units' tiles.
-__host__ __device__ inline int64_t share(int64_t total, int grid, int c) { return total * c / grid; }
+// First tile of CTA c's share of all units' tiles (rows are cut only where total x grid is far
+// inside 32 bits).
+__device__ __forceinline__ uint32_t share(uint32_t total, uint32_t grid, uint32_t c) { return total * c / grid; }
+
+// The it-th unit of this CTA.
+__device__ __forceinline__ Unit unit_at(const Params &P, int it) {
+    Unit u{-1, 0, 0, 0, -1};
+    uint32_t unit;
+    if (P.split) {
+        const uint32_t total = (uint32_t)P.units * P.tiles, end = share(total, gridDim.x, blockIdx.x + 1);
+        uint32_t t = share(total, gridDim.x, blockIdx.x);
+        unit = t / P.tiles + it;
+        if (it > 0) t = unit * P.tiles;
+        if (t >= end) return u;
+        u.tile0 = (int32_t)(t - unit * P.tiles);
+        u.tiles = (int32_t)min((uint32_t)(P.tiles - u.tile0), end - t);
+        if (u.tiles != P.tiles) u.part = 2 * blockIdx.x + (u.tile0 == 0 ? 1 : 0);
+    } else {
+        unit = blockIdx.x + (uint32_t)it * gridDim.x;       // units are below 2^26
+        if (unit >= (uint32_t)P.units) return u;
+        u.tiles = P.tiles;
+    }
+    u.row = (int32_t)(unit / P.head_blocks);
+    u.head0 = (int32_t)(unit - u.row * P.head_blocks) * 32;
+    return u;
+}
 
 // ---- scheduler -----------------------------------------------------------------------------------
 __device__ void scheduler_role(const Params &P, Tail *T, const Bars &bars) {
     const int lane = threadIdx.x & 31;
-    const int64_t total = P.units * P.tiles;
-    int64_t t = P.split ? share(total, gridDim.x, blockIdx.x) : (int64_t)blockIdx.x * P.tiles;
-    const int64_t end = P.split ? share(total, gridDim.x, blockIdx.x + 1) : total;
     for (int it = 0;; ++it) {
-        const bool more = t < end;
-        Unit u{-1, 0, 0, 0, -1};
-        if (more) {
-            const int64_t unit = t / P.tiles;
-            u.row = (int32_t)(unit / P.head_blocks);
-            u.head0 = (int32_t)(unit - (int64_t)u.row * P.head_blocks) * 32;
-            u.tile0 = (int32_t)(t - unit * P.tiles);
-            const int64_t left = P.split ? min((int64_t)P.tiles - u.tile0, end - t) : P.tiles;
-            u.tiles = (int32_t)left;
-            if (P.split && u.tiles != P.tiles) u.part = 2 * blockIdx.x + (u.tile0 == 0 ? 1 : 0);
-            t += P.split ? left : (int64_t)gridDim.x * P.tiles;
-            // tiles behind the last selected entry are left out
-            const int32_t *ir = P.indices + (int64_t)u.row * P.topk;
-            const int from = u.tile0 * kKeys, to = min((u.tile0 + u.tiles) * kKeys, P.topk);
-            if (__ldg(ir + to - 1) < 0) {
-                int last = -1;
+        const Unit u = unit_at(P, it);
+        if (u.row < 0) return;
+        // tiles behind the last selected entry are left out
+        const int32_t *ir = P.indices + (int64_t)u.row * P.topk;
+        const int from = u.tile0 * kKeys, to = min((u.tile0 + u.tiles) * kKeys, P.topk);
+        int tiles = u.tiles;
+        if (__ldg(ir + to - 1) < 0) {
+            int last = -1;
 #pragma unroll 8
-                for (int p = from + lane; p < to; p += 32)
-                    if (__ldg(ir + p) >= 0) last = p;
-                last = __reduce_max_sync(0xffffffffu, last);
-                u.tiles = last < from ? 0 : (last - from) / kKeys + 1;
-            }
+            for (int p = from + lane; p < to; p += 32)
+                if (__ldg(ir + p) >= 0) last = p;
+            last = __reduce_max_sync(0xffffffffu, last);
+            tiles = last < from ? 0 : (last - from) / kKeys + 1;
         }
         if (!wait_warp(bars.u_empty(it & 1), ((it >> 1) & 1) ^ 1, &T->abort_flag)) {
             T->abort_flag = 1;
             return;
         }
         if (lane == 0) {
-            T->unit[it & 1] = u;
+            T->tiles[it & 1] = tiles;
             mbar_arrive(bars.u_full(it & 1));
         }
         __syncwarp();
-        if (!more) return;
     }
 }
 
-// The it-th unit of this CTA, taken by a whole warp; false on giving up.
-__device__ __forceinline__ bool take_unit(Tail *T, const Bars &bars, int it, Unit *u) {
-    if (!wait_warp(bars.u_full(it & 1), (it >> 1) & 1, &T->abort_flag)) return false;
-    *u = T->unit[it & 1];
+// The tiles left of this CTA's it-th unit, for a whole warp; -1 on giving up.
+__device__ __forceinline__ int take_tiles(Tail *T, const Bars &bars, int it) {
+    if (!wait_warp(bars.u_full(it & 1), (it >> 1) & 1, &T->abort_flag)) return -1;
+    const int tiles = T->tiles[it & 1];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bars.u_empty(it & 1));
-    return true;
+    return __shfl_sync(0xffffffffu, tiles, 0);
 }
+
 // ---- q: normalised and split ---------------------------------------------------------------------
 template <int N>
 __device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bars) {
@@ -316,16 +333,14 @@ __device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &b
     Ring qr;
     int n = 0;                                  // units with tiles so far
     for (int it = 0;; ++it) {
-        Unit u;
-        if (!take_unit(T, bars, it, &u)) break;
+        const Unit u = unit_at(P, it);
         if (u.row < 0) return;
-        if (u.tiles == 0) continue;
-        if (!wait_warp(bars.q_empty(qr.idx), qr.phase ^ 1u, &T->abort_flag)) break;
-        uint8_t *qb = smem + qr.idx * P.q_bytes;
-        uint8_t *rb = qb + P.blocks * (2 * N * 128);
         const int heads = min(P.G - u.head0, N);
+        uint8_t *qb = nullptr, *rb = nullptr;
+        bool ok = true;
         for (int h0 = wp; h0 < N; h0 += 4 * R::kPrep) {
-            // four heads of the warp at once, so that their reads overlap
+            // four heads of the warp at once, so that their reads overlap; the first four are read
+            // while the unit's tiles and the buffer are not known yet
             uint4 v[4][2];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -338,6 +353,17 @@ __device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &b
                     if (h < heads && vec * 8 < P.Dm && idx_ok(qrow * P.Dm + vec * 8, (int64_t)P.rows * P.G * P.Dm, P.status))
                         v[t][i] = __ldg(reinterpret_cast<const uint4 *>(P.q + qrow * P.Dm) + vec);
                 }
+            }
+            if (h0 == wp) {
+                const int tiles = take_tiles(T, bars, it);
+                ok = tiles > 0 && wait_warp(bars.q_empty(qr.idx), qr.phase ^ 1u, &T->abort_flag);
+                if (!ok) {
+                    if (tiles == 0) break;
+                    T->abort_flag = 1;
+                    return;
+                }
+                qb = smem + qr.idx * P.q_bytes;
+                rb = qb + P.blocks * (2 * N * 128);
             }
             // the rope parts: 8 lanes a head
             if (P.has_rope) {
@@ -392,12 +418,12 @@ __device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &b
                 }
             }
         }
+        if (!ok) continue;                      // a unit without tiles
         fence_async_smem();
         mbar_arrive(bars.q_full(qr.idx));
         qr.next(P.q_bufs);
         ++n;
     }
-    T->abort_flag = 1;
 }
 
 // ---- gather ----------------------------------------------------------------------------------------
@@ -407,7 +433,7 @@ __device__ __forceinline__ int32_t entry_at(const Params &P, const int32_t *ir, 
     return pos < end ? __ldg(ir + pos) : -1;
 }
 __device__ __forceinline__ int32_t block_of(const Params &P, int64_t b, int32_t v) {
-    return P.block_table && v >= 0 && v < P.s2 ? __ldg(P.block_table + b * P.bt_stride + v / P.block_size) : 0;
+    return P.block_table && v >= 0 && v < P.s2 ? __ldg(P.block_table + b * P.bt_stride + P.by_block.div(v)) : 0;
 }
 // Cache row of position v, -1 where it selects nothing.
 __device__ __forceinline__ int32_t row_of(const Params &P, int64_t b, int32_t v, int32_t blk, uint32_t *err) {
@@ -421,7 +447,12 @@ __device__ __forceinline__ int32_t row_of(const Params &P, int64_t b, int32_t v,
         *err |= LI_DEVERR_TABLE;
         return -1;
     }
-    return blk * P.block_size + v % P.block_size;
+    return blk * P.block_size + v - P.by_block.div(v) * P.block_size;
+}
+
+// 4-byte copy into shared memory, tracked like every cp.async of the thread.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 template <int N>
@@ -433,26 +464,41 @@ __device__ void gather_role(const Params &P, const CUtensorMap *tm_codes, const 
     uint32_t err = 0;
     bool ok = true;
     for (int it = 0; ok; ++it) {
-        Unit u;
-        if (!take_unit(T, bars, it, &u)) { ok = false; break; }
+        // the first lookups do not wait for the scheduler
+        const Unit u = unit_at(P, it);
         if (u.row < 0) break;
-        if (u.tiles == 0) continue;
         const int32_t *ir = P.indices + (int64_t)u.row * P.topk;
-        const int64_t b = u.row / P.s1;
+        const int64_t b = P.by_s1.div(u.row);
         int pos = u.tile0 * kKeys + 32 * w + lane;
         const int end = min((u.tile0 + u.tiles) * kKeys, P.topk);
-        int32_t v0 = entry_at(P, ir, pos, end), v1 = entry_at(P, ir, pos + kKeys, end);
-        int32_t v2 = entry_at(P, ir, pos + 2 * kKeys, end);
-        int32_t blk = block_of(P, b, v0), blk1 = block_of(P, b, v1);
-        int32_t mine = row_of(P, b, v0, blk, &err);
-        if (mine >= 0 && !idx_ok(mine, P.key_rows, P.status)) mine = -1;
-        float d = mine >= 0 ? __ldg(P.descale + mine) : 0.0f;
-        for (int j = 0; j < u.tiles; ++j, tr.next(kTileRing)) {
+        int32_t va = entry_at(P, ir, pos, end), vb = entry_at(P, ir, pos + kKeys, end);
+        int32_t vc = entry_at(P, ir, pos + 2 * kKeys, end);
+        const int32_t blk0 = block_of(P, b, va);
+        int32_t blk_a = 0, blk_b = block_of(P, b, vb);
+        int32_t mine = row_of(P, b, va, blk0, &err);
+        va = vc;
+        const int tiles = take_tiles(T, bars, it);
+        if (tiles < 0) { ok = false; break; }
+        // One tile: its copies, then the lookups of the next (whose position and block are in v1 and
+        // blk1) and of the one after (position in v2); v1 takes the position of the third. Two tiles a
+        // turn with the registers' parts exchanged: a move of one still being read would wait for it.
+        const auto tile = [&](int32_t &v1, int32_t &blk1, int32_t &v2, int32_t &blk2) {
+            if (mine >= 0 && !idx_ok(mine, P.key_rows, P.status)) mine = -1;
+            // the key's scale for the softmax warps, checked there
+            float *d = &T->descale[tr.idx][32 * w + lane];
+            if (mine >= 0) {
+                cp_async4(smem_u32(d), P.descale + mine);
+                cp_async_arrive(bars.meta_full(tr.idx));
+            } else {
+                *d = __uint_as_float(kNoKey);
+                mbar_arrive(bars.meta_full(tr.idx));
+            }
+            __syncwarp();
             int32_t row[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) row[i] = __shfl_sync(0xffffffffu, mine, i);
             for (int c = P.has_rope ? -1 : 0; c < P.blocks; ++c, sr.next(P.slots)) {
-                if (!wait_warp(bars.slot_empty(sr.idx), sr.phase ^ 1u, &T->abort_flag)) { ok = false; break; }
+                if (!wait_warp(bars.slot_empty(sr.idx), sr.phase ^ 1u, &T->abort_flag)) return false;
                 const uint32_t to = dst + sr.idx * kSlot, full = bars.slot_full(sr.idx);
                 const CUtensorMap *map = c < 0 ? tm_rope : tm_codes;
                 const int32_t x = c < 0 ? 0 : 128 * c;
@@ -464,23 +510,20 @@ __device__ void gather_role(const Params &P, const CUtensorMap *tm_codes, const 
                 }
                 __syncwarp();
             }
-            if (!ok) break;
-            // a scale outside the range counts as no key: its codes meet weight 0
-            if (mine >= 0 && !(d >= kMinDescale && d <= kMaxDescale)) {
-                err |= LI_DEVERR_DESCALE;
-                d = 0.0f;
-            }
-            T->descale[tr.idx][32 * w + lane] = d;
-            mbar_arrive(bars.meta_full(tr.idx));
+            tr.next(kTileRing);
             pos += kKeys;
             mine = row_of(P, b, v1, blk1, &err);
-            if (mine >= 0 && !idx_ok(mine, P.key_rows, P.status)) mine = -1;
-            d = mine >= 0 ? __ldg(P.descale + mine) : 0.0f;
-            blk1 = block_of(P, b, v2);
-            v1 = v2;
-            v2 = entry_at(P, ir, pos + 2 * kKeys, end);
+            blk2 = block_of(P, b, v2);
+            v1 = entry_at(P, ir, pos + 2 * kKeys, end);
+            return true;
+        };
+        for (int j = 0; j < tiles && ok; j += 2) {
+            ok = tile(vb, blk_b, va, blk_a);
+            if (ok && j + 1 < tiles) ok = tile(va, blk_a, vb, blk_b);
         }
     }
+    // no copy may still be writing shared memory when the CTA leaves
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok) {
         T->abort_flag = 1;
         // copies of a tile that was not issued whole have no barrier to wait on: they land within
@@ -505,10 +548,9 @@ __device__ void qk_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
     Ring qr, sr;
     uint32_t kt = 0;
     for (int it = 0;; ++it) {
-        Unit u;
-        if (!take_unit(T, bars, it, &u)) break;
-        const int tiles = __shfl_sync(0xffffffffu, u.row < 0 ? -1 : u.tiles, 0);
-        if (tiles < 0) return;
+        if (unit_at(P, it).row < 0) return;
+        const int tiles = take_tiles(T, bars, it);
+        if (tiles < 0) break;
         if (tiles == 0) continue;
         if (!wait_warp(bars.q_full(qr.idx), qr.phase, &T->abort_flag)) break;
         const uint32_t qa = sbase + qr.idx * P.q_bytes;
@@ -552,10 +594,9 @@ __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
     Ring sr;
     uint32_t kt = 0, nu = 0;
     for (int it = 0;; ++it) {
-        Unit u;
-        if (!take_unit(T, bars, it, &u)) break;
-        const int tiles = __shfl_sync(0xffffffffu, u.row < 0 ? -1 : u.tiles, 0);
-        if (tiles < 0) return;
+        if (unit_at(P, it).row < 0) return;
+        const int tiles = take_tiles(T, bars, it);
+        if (tiles < 0) break;
         if (tiles == 0) continue;
         bool ok = true;
         for (int j = 0; j < tiles; ++j, ++kt) {
@@ -567,18 +608,23 @@ __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
             tc_fence_after();
             const uint64_t p = weights_desc<N>(sbase + P.p_off + (kt & 1u) * (2 * N * 128));
             if (P.has_rope) sr.next(P.slots);
-            for (int c = 0; c < P.blocks; ++c, sr.next(P.slots)) {
-                const uint64_t v = sw128_desc_mn(slots + sr.idx * kSlot, kSlot);
-                const uint32_t d = tmem + 2 * kSCols<N> + c * 2 * N;
-                if (elect_one()) {
+            // one elected lane for the whole tile
+            if (elect_one()) {
+                int slot = sr.idx;
+#pragma unroll 4
+                for (int c = 0; c < P.blocks; ++c) {
+                    const uint64_t v = sw128_desc_mn(slots + slot * kSlot, kSlot);
+                    const uint32_t d = tmem + 2 * kSCols<N> + c * 2 * N;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         umma_f8(d, v + k * (32 * 128 >> 4), p + k * (32 * 2 * N >> 4), idesc, (j | k) != 0);
-                    umma_commit(bars.slot_empty(sr.idx));
-                    if (c == P.blocks - 1) umma_commit(bars.p_empty(kt & 1u));
+                    umma_commit(bars.slot_empty(slot));
+                    if (++slot == P.slots) slot = 0;
                 }
-                __syncwarp();
+                umma_commit(bars.p_empty(kt & 1u));
             }
+            __syncwarp();
+            for (int c = 0; c < P.blocks; ++c) sr.next(P.slots);
         }
         if (!ok) break;
         ++nu;
@@ -607,8 +653,13 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
     Ring tr;
     uint32_t kt = 0;
     int nu = 0;
-    bool ok = true;
+    bool ok = true, bad = false;
     for (int it = 0;; ++it) {
+        const Unit u = unit_at(P, it);
+        if (u.row < 0) {
+            if (bad && P.status) atomicOr(P.status, LI_DEVERR_DESCALE);
+            return;
+        }
         // the group's warps agree on giving up here too (a vote below carries a failure on)
         bool got = mbar_wait(bars.u_full(it & 1), (it >> 1) & 1, abort_flag);
         got = __all_sync(0xffffffffu, got) && ok;
@@ -622,10 +673,9 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
             const int4 v = *reinterpret_cast<const int4 *>(T->vote[g][kt & 1]);
             if ((v.x | v.y | v.z | v.w) & 2) break;
         }
-        const Unit u = T->unit[it & 1];
+        const int tiles = T->tiles[it & 1];
         named_bar(bar_id, 128);                         // the vote slot is written again below
         if (lane == 0) mbar_arrive(bars.u_empty(it & 1));
-        if (u.row < 0) return;
         const int heads = min(P.G - u.head0 - H * g, H);        // may be <= 0
         const int64_t head_at = (int64_t)u.row * P.G + u.head0 + H * g;
         const bool row_ok = idx_ok(u.row, P.rows, P.status);
@@ -638,11 +688,16 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
         bool give_up = false, fresh = true;             // fresh: a head has no reference yet
         const float *ah = T->ah[nu & (kAhRing - 1)] + H * g;
         const float *ref = T->ref[g];
-        for (int j = 0; j < u.tiles; ++j, ++kt, tr.next(kTileRing)) {
+        for (int j = 0; j < tiles; ++j, ++kt, tr.next(kTileRing)) {
             const uint32_t b = kt & 1u;
             ok = ok && wait_warp(bars.meta_full(tr.idx), tr.phase, abort_flag);
-            // an entry that selects nothing has scale 0 and a weight of 2^-inf
-            const float d = ok ? T->descale[tr.idx][key] : 0.0f;
+            // an entry that selects nothing, or whose scale is out of range, has scale 0 and a weight
+            // of 2^-inf
+            float d = ok ? T->descale[tr.idx][key] : 0.0f;
+            if (!(d >= kMinDescale && d <= kMaxDescale)) {
+                bad |= ok && __float_as_uint(d) != kNoKey;
+                d = 0.0f;
+            }
             const float log2d = log2f(d), inv_d = d > 0.0f ? __frcp_rn(d) : 0.0f;
             ok = ok && wait_warp(bars.s_full(b), (kt >> 1) & 1u, abort_flag);
             float t[H];                                 // y - ref, the weights' exponents
@@ -778,7 +833,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
         }
         if (give_up) break;
         // the unit's sums and maxima over the group's 128 keys
-        if (u.tiles > 0) {
+        if (tiles > 0) {
             const float ws = transpose_reduce<false>(l, lane);
             float wm = 0.0f;
             if constexpr (kStats) wm = transpose_reduce<true>(mx, lane);
@@ -794,13 +849,13 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (u.tiles > 0) lds4(T->lsum[g][i], s4);
+            if (tiles > 0) lds4(T->lsum[g][i], s4);
             const float s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
             l[i] = u.part >= 0 ? 1.0f : s == 0.0f ? 0.0f : 1.0f / s;
         }
         if (q == 0 && lane < heads && row_ok && (u.part >= 0 || kStats)) {
             float s = 0.0f, m = -kInf, r = kNoRef;
-            if (u.tiles > 0) {
+            if (tiles > 0) {
                 float s4[4], m4[4];
                 lds4(T->lsum[g][lane], s4);
                 s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
@@ -825,7 +880,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
         if (u.part >= 0) {
             float *po = P.part_o + ((int64_t)u.part * N + H * g) * P.Dm + key;
             // a piece without keys is told by its sum of 0; nothing else of it is read
-            for (int c = 0; c < P.blocks && u.tiles > 0; ++c) {
+            for (int c = 0; c < P.blocks && tiles > 0; ++c) {
                 uint32_t hi[H], lo[H];
                 const uint32_t at = tmem + lanes + 2 * kSCols<N> + c * 2 * N + H * g;
                 tmem_ld_nowait(at, hi);
@@ -836,7 +891,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                     if (i < heads && row_ok)
                         po[(int64_t)i * P.Dm + 128 * c] = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
             }
-            if (u.tiles > 0) {
+            if (tiles > 0) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bars.o_empty());
@@ -847,7 +902,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
             for (int c = 0; c < 4; ++c) {
 #pragma unroll
                 for (int i = 0; i < H / 2; ++i) o[c][i] = 0u;
-                if (c < P.blocks && u.tiles > 0) {
+                if (c < P.blocks && tiles > 0) {
                     uint32_t hi[H], lo[H];
                     const uint32_t at = tmem + lanes + 2 * kSCols<N> + c * 2 * N + H * g;
                     tmem_ld_nowait(at, hi);
@@ -862,7 +917,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                     }
                 }
             }
-            if (u.tiles > 0) {
+            if (tiles > 0) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bars.o_empty());
@@ -1071,8 +1126,11 @@ bool cache_attn_plan(const li_cache_attn_args &a, CacheAttnPlan *p) {
     p->q_bytes = (uint32_t)(p->blocks * 2 * p->N * 128 + (a.Dr > 0 ? p->N * 128 : 0));
     const uint32_t p_bytes = 2u * 2u * p->N * 128u;
     p->slots = 0;
-    // two q buffers where two whole tiles still fit, so that a unit's q is ready when it starts
-    for (int bufs = 2; bufs >= 1; --bufs) {
+    const int64_t total = p->units * p->tiles;
+    p->split = p->units < 4 * (int64_t)sms && p->tiles > 1;
+    // whole units: two q buffers where two tiles still fit, so that a unit's q is ready when it starts;
+    // a CTA with a share has two or three units, and its keys want the room
+    for (int bufs = p->split ? 1 : 2; bufs >= 1; --bufs) {
         const uint32_t off = bufs * p->q_bytes;
         const uint32_t slot_off = (off + p_bytes + 1023u) / 1024u * 1024u;
         if (slot_off >= kTailOff) continue;
@@ -1091,8 +1149,6 @@ bool cache_attn_plan(const li_cache_attn_args &a, CacheAttnPlan *p) {
     uint32_t cols = 32;
     while (cols < (uint32_t)(8 * p->N + 2 * p->N * p->blocks)) cols <<= 1;
     p->tmem_cols = cols;
-    const int64_t total = p->units * p->tiles;
-    p->split = p->units < 4 * (int64_t)sms && p->tiles > 1;
     const int64_t most = p->split ? total : p->units;
     p->grid = (int)(most < sms ? most : sms);
     p->partial_floats = p->split ? (size_t)2 * p->grid * p->N * (a.Dm + 3) : 0;
@@ -1121,6 +1177,7 @@ cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnP
         P.block_table = a.block_table;
         P.bt_stride = a.block_table_stride;
         P.block_size = a.block_size;
+        P.by_block = FixedDiv(a.block_size);
         P.num_blocks = a.num_blocks;
         P.key_rows = (int64_t)a.num_blocks * a.block_size;
     } else {
@@ -1130,6 +1187,7 @@ cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnP
     P.scale = a.scale;
     P.rows = a.batch * a.s1;
     P.s1 = a.s1;
+    P.by_s1 = FixedDiv(a.s1);
     P.s2 = a.s2;
     P.G = a.G;
     P.Dm = a.Dm;
