@@ -103,6 +103,7 @@ constexpr int kNumBars = 17 + kTileRing + 2 * kMaxSlots;
 struct Tail {
     uint64_t bars[kNumBars];
     int32_t tiles[2];                           // the units' tiles left
+    uint32_t first, first_tile, end;            // split: first unit and its first tile, end of the share
     uint32_t tmem;
     volatile int abort_flag;
     alignas(16) int vote[2][2][4];              // [group][tile parity][warp]
@@ -133,7 +134,7 @@ struct Params {
     int32_t has_rope, blocks, head_blocks, tiles, split;
     int32_t q_bufs, slots;
     uint32_t q_bytes, p_off, slot_off, tmem_cols;
-    FixedDiv by_block, by_s1;
+    FixedDiv by_block, by_s1, by_heads;
 };
 
 struct Ring {
@@ -144,8 +145,15 @@ struct Ring {
     }
 };
 
+// Bounded wait of a whole warp, with one answer for all lanes. What follows a first try that fails is
+// out of line: the kernel has some thirty waits, and its loops compete for the instruction caches.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    return mbar_wait(bar, parity, abort_flag);
+}
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+    bool ok = mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) ok = __all_sync(0xffffffffu, wait_long(bar, parity, abort_flag));
+    return ok;
 }
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                         uint32_t accumulate) {
@@ -176,18 +184,12 @@ __device__ __forceinline__ float exp2_(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ uint32_t e4m3x2(__half2 v) {
-    return __nv_cvt_halfraw2_to_fp8x2((__half2_raw)v, __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ __half2 e4m3x2_h2(uint32_t v) {
-    return __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3));
-}
-__device__ __forceinline__ float2 e4m3x2_f32(uint32_t v) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3);
-    return __half22float2(__half2(h));
+// x = hi + lo / 16 with both parts in E4M3, two elements each (4 bits and the next 4, with a sign).
+__device__ __forceinline__ void split_e4m3(__half2 x, uint32_t *hi, uint32_t *lo) {
+    *hi = __nv_cvt_halfraw2_to_fp8x2((__half2_raw)x, __NV_SATFINITE, __NV_E4M3);
+    const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)*hi, __NV_E4M3));
+    const __half2 rest = __hfma2(h, __float2half2_rn(-16.0f), __hmul2(x, __float2half2_rn(16.0f)));
+    *lo = __nv_cvt_halfraw2_to_fp8x2((__half2_raw)rest, __NV_SATFINITE, __NV_E4M3);
 }
 // n consecutive fp32 columns of this thread's TMEM lane, without the wait.
 __device__ __forceinline__ void tmem_ld_nowait(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16_nowait(taddr, r); }
@@ -263,25 +265,22 @@ __device__ __forceinline__ float transpose_reduce(const float (&v)[H], int lane)
 __device__ __forceinline__ uint32_t share(uint32_t total, uint32_t grid, uint32_t c) { return total * c / grid; }
 
 // The it-th unit of this CTA.
-__device__ __forceinline__ Unit unit_at(const Params &P, int it) {
-    Unit u{-1, 0, 0, 0, -1};
+__device__ __forceinline__ Unit unit_at(const Params &P, const Tail *T, int it) {
+    Unit u{-1, 0, 0, P.tiles, -1};
     uint32_t unit;
     if (P.split) {
-        const uint32_t total = (uint32_t)P.units * P.tiles, end = share(total, gridDim.x, blockIdx.x + 1);
-        uint32_t t = share(total, gridDim.x, blockIdx.x);
-        unit = t / P.tiles + it;
-        if (it > 0) t = unit * P.tiles;
-        if (t >= end) return u;
-        u.tile0 = (int32_t)(t - unit * P.tiles);
-        u.tiles = (int32_t)min((uint32_t)(P.tiles - u.tile0), end - t);
+        unit = T->first + it;
+        const uint32_t t = unit * P.tiles;              // the unit's first tile
+        if (t >= T->end) return u;
+        u.tile0 = it == 0 ? (int32_t)T->first_tile : 0;
+        u.tiles = (int32_t)(min((uint32_t)P.tiles, T->end - t) - u.tile0);
         if (u.tiles != P.tiles) u.part = 2 * blockIdx.x + (u.tile0 == 0 ? 1 : 0);
     } else {
         unit = blockIdx.x + (uint32_t)it * gridDim.x;       // units are below 2^26
         if (unit >= (uint32_t)P.units) return u;
-        u.tiles = P.tiles;
     }
-    u.row = (int32_t)(unit / P.head_blocks);
-    u.head0 = (int32_t)(unit - u.row * P.head_blocks) * 32;
+    u.row = P.by_heads.div((int32_t)unit);
+    u.head0 = ((int32_t)unit - u.row * P.head_blocks) * 32;
     return u;
 }
 
@@ -289,7 +288,7 @@ __device__ __forceinline__ Unit unit_at(const Params &P, int it) {
 __device__ void scheduler_role(const Params &P, Tail *T, const Bars &bars) {
     const int lane = threadIdx.x & 31;
     for (int it = 0;; ++it) {
-        const Unit u = unit_at(P, it);
+        const Unit u = unit_at(P, T, it);
         if (u.row < 0) return;
         // tiles behind the last selected entry are left out
         const int32_t *ir = P.indices + (int64_t)u.row * P.topk;
@@ -333,65 +332,59 @@ __device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &b
     Ring qr;
     int n = 0;                                  // units with tiles so far
     for (int it = 0;; ++it) {
-        const Unit u = unit_at(P, it);
+        const Unit u = unit_at(P, T, it);
         if (u.row < 0) return;
         const int heads = min(P.G - u.head0, N);
-        uint8_t *qb = nullptr, *rb = nullptr;
-        bool ok = true;
-        for (int h0 = wp; h0 < N; h0 += 4 * R::kPrep) {
+        const int64_t row0 = (int64_t)u.row * P.G + u.head0;
+        uint8_t *qb = nullptr;
+        bool some = true;
+        for (int h0 = wp; h0 < N && some; h0 += 4 * R::kPrep) {
             // four heads of the warp at once, so that their reads overlap; the first four are read
             // while the unit's tiles and the buffer are not known yet
-            uint4 v[4][2];
+            uint4 v[4][2], rope = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int h = h0 + t * R::kPrep;
-                const int64_t qrow = (int64_t)u.row * P.G + u.head0 + h;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int vec = lane + 32 * i;          // 8 elements
                     v[t][i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (h < heads && vec * 8 < P.Dm && idx_ok(qrow * P.Dm + vec * 8, (int64_t)P.rows * P.G * P.Dm, P.status))
-                        v[t][i] = __ldg(reinterpret_cast<const uint4 *>(P.q + qrow * P.Dm) + vec);
+                    if (h < heads && vec * 8 < P.Dm && idx_ok((row0 + h) * P.Dm + vec * 8, (int64_t)P.rows * P.G * P.Dm, P.status))
+                        v[t][i] = __ldg(reinterpret_cast<const uint4 *>(P.q + (row0 + h) * P.Dm) + vec);
                 }
             }
+            // the rope parts: 8 lanes a head
+            const int rh = h0 + (lane >> 3) * R::kPrep, piece = lane & 7;
+            if (P.has_rope && rh < heads && idx_ok((row0 + rh) * 64 + piece * 8, (int64_t)P.rows * P.G * 64, P.status))
+                rope = __ldg(reinterpret_cast<const uint4 *>(P.q_rope + (row0 + rh) * 64) + piece);
             if (h0 == wp) {
                 const int tiles = take_tiles(T, bars, it);
-                ok = tiles > 0 && wait_warp(bars.q_empty(qr.idx), qr.phase ^ 1u, &T->abort_flag);
-                if (!ok) {
-                    if (tiles == 0) break;
+                some = tiles != 0;
+                if (!some) break;
+                if (tiles < 0 || !wait_warp(bars.q_empty(qr.idx), qr.phase ^ 1u, &T->abort_flag)) {
                     T->abort_flag = 1;
                     return;
                 }
                 qb = smem + qr.idx * P.q_bytes;
-                rb = qb + P.blocks * (2 * N * 128);
             }
-            // the rope parts: 8 lanes a head
-            if (P.has_rope) {
-                const int h = h0 + (lane >> 3) * R::kPrep, piece = lane & 7;
-                const int64_t qrow = (int64_t)u.row * P.G + u.head0 + h;
-                uint4 r = make_uint4(0u, 0u, 0u, 0u);
-                if (h < heads && idx_ok(qrow * 64 + piece * 8, (int64_t)P.rows * P.G * 64, P.status))
-                    r = __ldg(reinterpret_cast<const uint4 *>(P.q_rope + qrow * 64) + piece);
-                *reinterpret_cast<uint4 *>(rb + h * 128 + ((piece ^ (h & 7)) << 4)) = r;
-            }
+            if (P.has_rope)
+                *reinterpret_cast<uint4 *>(qb + P.blocks * (2 * N * 128) + rh * 128 + ((piece ^ (rh & 7)) << 4)) = rope;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int h = h0 + t * R::kPrep;
-                float amax = 0.0f;
+                __nv_bfloat162 m2 = __float2bfloat162_rn(0.0f);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t w[4] = {v[t][i].x, v[t][i].y, v[t][i].z, v[t][i].w};
+                    const __nv_bfloat162 *w = reinterpret_cast<const __nv_bfloat162 *>(&v[t][i]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float a = fabsf(bf16_lo(w[j])), b = fabsf(bf16_hi(w[j]));
-                        if (a < kInf) amax = fmaxf(amax, a);
-                        if (b < kInf) amax = fmaxf(amax, b);
-                    }
+                    for (int j = 0; j < 4; ++j) m2 = __hmax2(m2, __habs2(w[j]));
                 }
-                amax = warp_max(amax);
-                // f = 2^(7 - exponent of amax): the largest element lands in [128, 256)
+                const float amax = warp_max(fmaxf(__low2float(m2), __high2float(m2)));
+                // f = 2^(7 - exponent of amax): the largest element lands in [128, 256). An infinity
+                // has no code: f is NaN then, so that the head's result shows it
                 const int e = max((int)(__float_as_uint(amax) >> 23), 8);   // biased; 8 keeps f finite
-                const float f = amax > 0.0f ? __uint_as_float((uint32_t)(127 + 7 + 127 - e) << 23) : 1.0f;
+                float f = amax > 0.0f ? __uint_as_float((uint32_t)(127 + 7 + 127 - e) << 23) : 1.0f;
+                if (amax == kInf) f = __int_as_float(0x7fc00000);
                 if (lane == 0) T->ah[n & (kAhRing - 1)][h] = P.scale * kLog2e / f;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -401,13 +394,9 @@ __device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &b
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        // an infinity has no code: NaN, so that the head's result shows it
-                        float a = bf16_lo(w[j]) * f, b = bf16_hi(w[j]) * f;
-                        if (!(fabsf(a) < kInf)) a = __int_as_float(0x7fc00000);
-                        if (!(fabsf(b) < kInf)) b = __int_as_float(0x7fc00000);
-                        hi[j] = e4m3x2(a, b);
-                        const float2 r = e4m3x2_f32(hi[j]);
-                        lo[j] = e4m3x2((a - r.x) * 16.0f, (b - r.y) * 16.0f);
+                        // fp16 holds q f exactly down to 2^-14, and what lies below has no lo part
+                        const __half2 x = __floats2half2_rn(bf16_lo(w[j]) * f, bf16_hi(w[j]) * f);
+                        split_e4m3(x, &hi[j], &lo[j]);
                     }
                     const int off = (vec * 8) & 127, b = vec >> 4;
                     const uint32_t at = (uint32_t)(b * 2 * N * 128 + (((off >> 4) ^ (h & 7)) << 4) + (off & 8));
@@ -418,7 +407,7 @@ __device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &b
                 }
             }
         }
-        if (!ok) continue;                      // a unit without tiles
+        if (!some) continue;                    // a unit without tiles
         fence_async_smem();
         mbar_arrive(bars.q_full(qr.idx));
         qr.next(P.q_bufs);
@@ -465,7 +454,7 @@ __device__ void gather_role(const Params &P, const CUtensorMap *tm_codes, const 
     bool ok = true;
     for (int it = 0; ok; ++it) {
         // the first lookups do not wait for the scheduler
-        const Unit u = unit_at(P, it);
+        const Unit u = unit_at(P, T, it);
         if (u.row < 0) break;
         const int32_t *ir = P.indices + (int64_t)u.row * P.topk;
         const int64_t b = P.by_s1.div(u.row);
@@ -548,7 +537,7 @@ __device__ void qk_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
     Ring qr, sr;
     uint32_t kt = 0;
     for (int it = 0;; ++it) {
-        if (unit_at(P, it).row < 0) return;
+        if (unit_at(P, T, it).row < 0) return;
         const int tiles = take_tiles(T, bars, it);
         if (tiles < 0) break;
         if (tiles == 0) continue;
@@ -594,7 +583,7 @@ __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
     Ring sr;
     uint32_t kt = 0, nu = 0;
     for (int it = 0;; ++it) {
-        if (unit_at(P, it).row < 0) return;
+        if (unit_at(P, T, it).row < 0) return;
         const int tiles = take_tiles(T, bars, it);
         if (tiles < 0) break;
         if (tiles == 0) continue;
@@ -655,14 +644,13 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
     int nu = 0;
     bool ok = true, bad = false;
     for (int it = 0;; ++it) {
-        const Unit u = unit_at(P, it);
+        const Unit u = unit_at(P, T, it);
         if (u.row < 0) {
             if (bad && P.status) atomicOr(P.status, LI_DEVERR_DESCALE);
             return;
         }
         // the group's warps agree on giving up here too (a vote below carries a failure on)
-        bool got = mbar_wait(bars.u_full(it & 1), (it >> 1) & 1, abort_flag);
-        got = __all_sync(0xffffffffu, got) && ok;
+        const bool got = wait_warp(bars.u_full(it & 1), (it >> 1) & 1, abort_flag) && ok;
         if (lane == 0) T->vote[g][kt & 1][q] = got ? 0 : 2;
         if (q == 0 && lane < H) {
             T->ref[g][lane] = 0.0f;
@@ -779,6 +767,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 if (j > 0) {
                     ok = ok && wait_warp(bars.p_empty(b ^ 1u), ((kt - 1) >> 1) & 1u, abort_flag);
                     tc_fence_after();
+#pragma unroll 1
                     for (int c = 0; c < P.blocks; ++c) {
                         const uint32_t o = tmem + lanes + 2 * kSCols<N> + c * 2 * N + H * g;
                         uint32_t hi[H], lo[H];
@@ -808,10 +797,8 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 const float p0 = exp2_(t[i]), p1 = exp2_(t[i + 1]);
                 l[i] = fmaf(p0, inv_d, l[i]);
                 l[i + 1] = fmaf(p1, inv_d, l[i + 1]);
-                const __half2 p = __floats2half2_rn(p0, p1);
-                const uint32_t h8 = e4m3x2(p);
-                const __half2 rem = __hfma2(e4m3x2_h2(h8), __float2half2_rn(-16.0f), __hmul2(p, __float2half2_rn(16.0f)));
-                const uint32_t l8 = e4m3x2(rem);
+                uint32_t h8, l8;
+                split_e4m3(__floats2half2_rn(p0, p1), &h8, &l8);
                 if (i & 2) {
                     hi[i / 4] |= h8 << 16;
                     lo[i / 4] |= l8 << 16;
@@ -875,12 +862,17 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 P.ssum[head_at + lane] = m > -kInf ? s * exp2_(r - m) : s;
             }
         }
-        // O out of TMEM, whole units as bf16 (two heads a register), so that the next unit's product
-        // can start before the stores
-        if (u.part >= 0) {
-            float *po = P.part_o + ((int64_t)u.part * N + H * g) * P.Dm + key;
-            // a piece without keys is told by its sum of 0; nothing else of it is read
-            for (int c = 0; c < P.blocks && tiles > 0; ++c) {
+        // O out of TMEM: pieces of a unit as they are in fp32, whole units normalised as bf16
+        float *po = P.part_o + ((int64_t)u.part * N + H * g) * P.Dm + key;
+        // neighbouring lanes exchange halves: an even lane stores two dims of the even heads, an odd
+        // lane of the odd heads
+        uint16_t *out = P.out + (head_at + (lane & 1)) * P.Dm + (key & ~1);
+#pragma unroll 1
+        for (int c = 0; c < P.blocks; ++c, po += 128, out += 128) {
+            float o[H];
+#pragma unroll
+            for (int i = 0; i < H; ++i) o[i] = 0.0f;
+            if (tiles > 0) {
                 uint32_t hi[H], lo[H];
                 const uint32_t at = tmem + lanes + 2 * kSCols<N> + c * 2 * N + H * g;
                 tmem_ld_nowait(at, hi);
@@ -888,51 +880,26 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < H; ++i)
-                    if (i < heads && row_ok)
-                        po[(int64_t)i * P.Dm + 128 * c] = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
-            }
-            if (tiles > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.o_empty());
-            }
-        } else {
-            uint32_t o[4][H / 2];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-#pragma unroll
-                for (int i = 0; i < H / 2; ++i) o[c][i] = 0u;
-                if (c < P.blocks && tiles > 0) {
-                    uint32_t hi[H], lo[H];
-                    const uint32_t at = tmem + lanes + 2 * kSCols<N> + c * 2 * N + H * g;
-                    tmem_ld_nowait(at, hi);
-                    tmem_ld_nowait(at + N, lo);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < H; i += 2) {
-                        const float a = l[i] * fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
-                        const float b = l[i + 1] * fmaf(__uint_as_float(lo[i + 1]), 0.0625f, __uint_as_float(hi[i + 1]));
-                        const __nv_bfloat162 ab = __floats2bfloat162_rn(a, b);
-                        o[c][i / 2] = *reinterpret_cast<const uint32_t *>(&ab);
-                    }
+                    o[i] = l[i] * fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
+                if (c == P.blocks - 1) {                // the next unit's product may start
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars.o_empty());
                 }
             }
-            if (tiles > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.o_empty());
-            }
-            // neighbouring lanes exchange halves: an even lane stores two dims of the even heads, an
-            // odd lane of the odd heads
-            uint16_t *po = P.out + head_at * P.Dm + (key & ~1) + (int64_t)(lane & 1) * P.Dm;
+            if (u.part >= 0) {
+                // a piece without keys is told by its sum of 0; nothing else of it is read
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+                for (int i = 0; i < H; ++i)
+                    if (i < heads && tiles > 0 && row_ok) po[(int64_t)i * P.Dm] = o[i];
+            } else {
 #pragma unroll
-                for (int i = 0; i < H / 2; ++i) {
-                    const uint32_t mine = o[c][i], theirs = __shfl_xor_sync(0xffffffffu, mine, 1);
+                for (int i = 0; i < H; i += 2) {
+                    const __nv_bfloat162 ab = __floats2bfloat162_rn(o[i], o[i + 1]);
+                    const uint32_t mine = *reinterpret_cast<const uint32_t *>(&ab);
+                    const uint32_t theirs = __shfl_xor_sync(0xffffffffu, mine, 1);
                     const uint32_t v = lane & 1 ? __byte_perm(theirs, mine, 0x7632) : __byte_perm(mine, theirs, 0x5410);
-                    if (c < P.blocks && 2 * i + (lane & 1) < heads && row_ok)
-                        *reinterpret_cast<uint32_t *>(po + (int64_t)(2 * i) * P.Dm + 128 * c) = v;
+                    if (i + (lane & 1) < heads && row_ok) *reinterpret_cast<uint32_t *>(out + (int64_t)i * P.Dm) = v;
                 }
             }
         }
@@ -972,6 +939,12 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(
             mbar_init(bars.slot_empty(i), 1);
         }
         T->abort_flag = 0;
+        if (P.split) {
+            const uint32_t total = (uint32_t)P.units * P.tiles, t = share(total, gridDim.x, blockIdx.x);
+            T->first = t / P.tiles;
+            T->first_tile = t - T->first * P.tiles;
+            T->end = share(total, gridDim.x, blockIdx.x + 1);
+        }
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_codes)) : "memory");
         if (P.has_rope) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_rope)) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1195,6 +1168,7 @@ cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnP
     P.has_rope = a.Dr > 0;
     P.blocks = p.blocks;
     P.head_blocks = p.head_blocks;
+    P.by_heads = FixedDiv(p.head_blocks);
     P.tiles = p.tiles;
     P.split = p.split;
     P.q_bufs = p.q_bufs;

@@ -12,7 +12,8 @@ namespace li {
 struct FixedDiv {
     uint32_t m = 0;
     int32_t shift = -1;                 // l - 1, -1 for d = 1
-    __host__ explicit FixedDiv(uint32_t d = 1) {
+    __host__ FixedDiv() {}
+    __host__ explicit FixedDiv(uint32_t d) {
         if (d <= 1) return;
         int l = 0;
         while (((uint64_t)1 << l) < d) ++l;
