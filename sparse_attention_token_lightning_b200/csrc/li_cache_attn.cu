@@ -26,9 +26,9 @@
 //             maxima reduced and O rescaled. Weights below 2^-18 of the largest may round to 0
 //   prep      the next unit's q: normalised, split and stored in the MMA layout
 //   gather    looks up each selected key's cache row, keeps its scale for the softmax warps and
-//             has TMA gather codes and rope part, four rows an instruction, into 16 KB slots (128
-//             keys x 128 bytes, 128-byte swizzle); an entry that selects nothing is row -1, which
-//             reads as zeros
+//             copies codes and rope part with cp.async into 16 KB slots (128 keys x 128 bytes,
+//             128-byte swizzle); rows that select nothing are zero-filled. TMA's gather of four rows
+//             took %TMA%
 //   scheduler the CTA's units;  qk / pv: one thread each issues the two products
 // Every wait is bounded in time; on expiry the kernel records LI_DEVERR_TIMEOUT and returns. The
 // softmax warps of a group agree on giving up (the vote carries it), so none is left at a barrier.
@@ -150,6 +150,11 @@ struct Ring {
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
     return mbar_wait(bar, parity, abort_flag);
 }
+// Every lane for itself (the loops that issue copies and products: a vote per wait costs them more
+// than the wait); the lanes may differ in their answer, and the caller lets them agree later.
+__device__ __forceinline__ bool wait_lane(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag);
+}
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
     bool ok = mbar_try_wait(bar, parity);
     if (!__all_sync(0xffffffffu, ok)) ok = __all_sync(0xffffffffu, wait_long(bar, parity, abort_flag));
@@ -169,15 +174,9 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
 }
-// Four rows of a [rows][x] map, 128 bytes of each from column x on, to four 128-byte rows of shared
-// memory; rows outside the map (-1) read as zeros.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t x,
-                                            int32_t r0, int32_t r1, int32_t r2, int32_t r3) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
-        : "memory");
+// 16-byte copy, `bytes` (0 or 16) of them read and the rest filled with zeros.
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ float exp2_(float x) {
     float y;
@@ -445,10 +444,12 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
 }
 
 template <int N>
-__device__ void gather_role(const Params &P, const CUtensorMap *tm_codes, const CUtensorMap *tm_rope,
-                            uint8_t *smem, Tail *T, const Bars &bars) {
+__device__ void gather_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bars) {
     const int w = (threadIdx.x >> 5) - Roles<N>::kGather0, lane = threadIdx.x & 31;
-    const uint32_t dst = smem_u32(smem) + P.slot_off + 32 * w * 128;    // this warp's 32 keys of a slot
+    const int piece = lane & 7, sub = lane >> 3;        // this lane copies keys 32 w + sub + 4 i
+    // 16-byte piece of row key in a swizzled slot; key & 7 is sub + 4 (i & 1)
+    const uint32_t dst = smem_u32(smem) + P.slot_off + (32 * w + sub) * 128;
+    const uint32_t even = (uint32_t)((piece ^ sub) << 4), odd = (uint32_t)((piece ^ (sub + 4)) << 4);
     Ring sr, tr;
     uint32_t err = 0;
     bool ok = true;
@@ -483,22 +484,47 @@ __device__ void gather_role(const Params &P, const CUtensorMap *tm_codes, const 
                 mbar_arrive(bars.meta_full(tr.idx));
             }
             __syncwarp();
-            int32_t row[32];
+            // the eight rows of this lane: where they start, and 16 bytes of each piece or none
+            const uint8_t *row[8];
+            uint32_t size[8];
+            bool there = true;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) row[i] = __shfl_sync(0xffffffffu, mine, i);
-            for (int c = P.has_rope ? -1 : 0; c < P.blocks; ++c, sr.next(P.slots)) {
-                if (!wait_warp(bars.slot_empty(sr.idx), sr.phase ^ 1u, &T->abort_flag)) return false;
-                const uint32_t to = dst + sr.idx * kSlot, full = bars.slot_full(sr.idx);
-                const CUtensorMap *map = c < 0 ? tm_rope : tm_codes;
-                const int32_t x = c < 0 ? 0 : 128 * c;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(full, 32u * 128u);
+            for (int i = 0; i < 8; ++i) {
+                const int32_t r = __shfl_sync(0xffffffffu, mine, sub + 4 * i);
+                size[i] = r < 0 ? 0u : 16u;
+                row[i] = P.codes + (int64_t)max(r, 0) * P.Dm + piece * 16;
+            }
+            if (P.has_rope) {
+                const uint8_t *rope[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int32_t r = __shfl_sync(0xffffffffu, mine, sub + 4 * i);
+                    rope[i] = reinterpret_cast<const uint8_t *>(P.k_rope) + (int64_t)max(r, 0) * 128 + piece * 16;
+                }
+                there = wait_lane(bars.slot_empty(sr.idx), sr.phase ^ 1u, &T->abort_flag);
+                if (there) {
+                    const uint32_t to = dst + sr.idx * kSlot;
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        tma_gather4(to + i * 512, map, full, x, row[4 * i], row[4 * i + 1], row[4 * i + 2], row[4 * i + 3]);
+                        cp_async16_zfill(to + i * 512 + (i & 1 ? odd : even), rope[i], size[i]);
+                    cp_async_arrive(bars.slot_full(sr.idx));
                 }
-                __syncwarp();
+                sr.next(P.slots);
             }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (c >= P.blocks) break;
+                if (!there) break;              // a slot that is not free is not written
+                there = wait_lane(bars.slot_empty(sr.idx), sr.phase ^ 1u, &T->abort_flag);
+                if (!there) break;
+                const uint32_t to = dst + sr.idx * kSlot;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    cp_async16_zfill(to + i * 512 + (i & 1 ? odd : even), row[i] + 128 * c, size[i]);
+                cp_async_arrive(bars.slot_full(sr.idx));
+                sr.next(P.slots);
+            }
+            if (!__all_sync(0xffffffffu, there)) return false;
             tr.next(kTileRing);
             pos += kKeys;
             mine = row_of(P, b, v1, blk1, &err);
@@ -513,13 +539,7 @@ __device__ void gather_role(const Params &P, const CUtensorMap *tm_codes, const 
     }
     // no copy may still be writing shared memory when the CTA leaves
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (!ok) {
-        T->abort_flag = 1;
-        // copies of a tile that was not issued whole have no barrier to wait on: they land within
-        // microseconds, so the CTA stays for a hundred of them before it gives its memory up
-        const unsigned long long t0 = globaltimer();
-        while (globaltimer() - t0 < 100000ull) {}
-    }
+    if (!ok) T->abort_flag = 1;
     if (err && P.status) atomicOr(P.status, err);
 }
 
@@ -546,27 +566,43 @@ __device__ void qk_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
         bool ok = true;
         for (int j = 0; j < tiles && ok; ++j, ++kt) {
             const uint32_t b = kt & 1u, d = tmem + b * kSCols<N>;
-            ok = wait_warp(bars.s_empty(b), ((kt >> 1) & 1u) ^ 1u, &T->abort_flag);
-            // a slot's part of the product starts when the slot is there; the rope part comes first
-            for (int c = P.has_rope ? -1 : 0; c < P.blocks && ok; ++c, sr.next(P.slots)) {
-                ok = wait_warp(bars.slot_full(sr.idx), sr.phase, &T->abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t a = sw128_desc(slots + sr.idx * kSlot);
-                const uint64_t q = sw128_desc(qa + (c < 0 ? P.blocks : c) * kQBlock);
-                if (elect_one()) {
-                    if (c < 0) {
+            // one lane for the whole tile, its waits included; a slot's part of the product starts when
+            // the slot is there, the rope part first
+            if (elect_one()) {
+                int slot = sr.idx;
+                uint32_t phase = sr.phase;
+                const auto next = [&] {
+                    if (++slot == P.slots) { slot = 0; phase ^= 1u; }
+                };
+                ok = wait_lane(bars.s_empty(b), ((kt >> 1) & 1u) ^ 1u, &T->abort_flag);
+                if (P.has_rope && ok) {
+                    ok = wait_lane(bars.slot_full(slot), phase, &T->abort_flag);
+                    fence_async_smem();         // the gathered rows, for the async proxy
+                    tc_fence_after();
+                    const uint64_t a = sw128_desc(slots + slot * kSlot), q = sw128_desc(qa + P.blocks * kQBlock);
+                    if (ok) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) umma_f16(d + 2 * N, a + 2 * k, q + 2 * k, idesc16, k > 0);
-                        umma_commit(bars.slot_empty(sr.idx));
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) umma_f8(d, a + 2 * k, q + 2 * k, idesc8, (c | k) != 0);
-                        if (c == P.blocks - 1) umma_commit(bars.s_full(b));
+                        umma_commit(bars.slot_empty(slot));
                     }
+                    next();
                 }
-                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c >= P.blocks || !ok) break;
+                    ok = wait_lane(bars.slot_full(slot), phase, &T->abort_flag);
+                    if (!ok) break;
+                    fence_async_smem();
+                    tc_fence_after();
+                    const uint64_t a = sw128_desc(slots + slot * kSlot), q = sw128_desc(qa + c * kQBlock);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) umma_f8(d, a + 2 * k, q + 2 * k, idesc8, (c | k) != 0);
+                    next();
+                }
+                if (ok) umma_commit(bars.s_full(b));
             }
+            ok = __all_sync(0xffffffffu, ok);
+            for (int c = P.has_rope ? -1 : 0; c < P.blocks; ++c) sr.next(P.slots);
         }
         if (!ok) break;
         if (elect_one()) umma_commit(bars.q_empty(qr.idx));
@@ -678,7 +714,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
         const float *ref = T->ref[g];
         for (int j = 0; j < tiles; ++j, ++kt, tr.next(kTileRing)) {
             const uint32_t b = kt & 1u;
-            ok = ok && wait_warp(bars.meta_full(tr.idx), tr.phase, abort_flag);
+            ok = ok && wait_lane(bars.meta_full(tr.idx), tr.phase, abort_flag);
             // an entry that selects nothing, or whose scale is out of range, has scale 0 and a weight
             // of 2^-inf
             float d = ok ? T->descale[tr.idx][key] : 0.0f;
@@ -687,8 +723,9 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 d = 0.0f;
             }
             const float log2d = log2f(d), inv_d = d > 0.0f ? __frcp_rn(d) : 0.0f;
-            ok = ok && wait_warp(bars.s_full(b), (kt >> 1) & 1u, abort_flag);
+            ok = ok && wait_lane(bars.s_full(b), (kt >> 1) & 1u, abort_flag);
             float t[H];                                 // y - ref, the weights' exponents
+            __syncwarp();
             tc_fence_after();
             {
                 uint32_t hi[H], lo[H], rp[H];
@@ -724,7 +761,8 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 }
             }
             const bool any = __any_sync(0xffffffffu, top > kTop || (fresh && d > 0.0f));
-            if (lane == 0) T->vote[g][b][q] = (any ? 1 : 0) | (ok ? 0 : 2);
+            const bool all = __all_sync(0xffffffffu, ok);
+            if (lane == 0) T->vote[g][b][q] = (any ? 1 : 0) | (all ? 0 : 2);
             named_bar(bar_id, 128);
             const int4 v4 = *reinterpret_cast<const int4 *>(T->vote[g][b]);
             const int v = v4.x | v4.y | v4.z | v4.w;
@@ -765,7 +803,8 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                     }
                 }
                 if (j > 0) {
-                    ok = ok && wait_warp(bars.p_empty(b ^ 1u), ((kt - 1) >> 1) & 1u, abort_flag);
+                    ok = ok && wait_lane(bars.p_empty(b ^ 1u), ((kt - 1) >> 1) & 1u, abort_flag);
+                    __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < P.blocks; ++c) {
@@ -789,7 +828,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
             // p_empty(i) completes with the value product of every second tile: it frees that tile's
             // weights, and O holds all tiles up to it. A wait for tile t is sound because the wait
             // below for tile t - 2 came before (a parity says nothing of phases further back)
-            ok = ok && wait_warp(bars.p_empty(b), ((kt >> 1) & 1u) ^ 1u, abort_flag);
+            ok = ok && wait_lane(bars.p_empty(b), ((kt >> 1) & 1u) ^ 1u, abort_flag);
             // weights as hi + lo / 16, by way of fp16 (11 bits); a key's row of the operand
             uint32_t hi[H / 4], lo[H / 4];
 #pragma unroll
@@ -828,7 +867,8 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 T->lsum[g][lane / (32 / H)][q] = ws;
                 if (kStats) T->mx[g][lane / (32 / H)][q] = wm;
             }
-            ok = ok && wait_warp(bars.p_empty((kt - 1) & 1u), ((kt - 1) >> 1) & 1u, abort_flag);
+            ok = ok && wait_lane(bars.p_empty((kt - 1) & 1u), ((kt - 1) >> 1) & 1u, abort_flag);
+            __syncwarp();
             tc_fence_after();
             named_bar(bar_id, 128);
             ++nu;
@@ -909,9 +949,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
 }
 
 template <int N, bool kStats>
-__global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(
-    const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_rope,
-    const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const __grid_constant__ Params P) {
     using R = Roles<N>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5;
@@ -935,7 +973,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(
         mbar_init(bars.o_empty(), R::kSoft);
         for (int i = 0; i < kTileRing; ++i) mbar_init(bars.meta_full(i), 32 * kGatherWarps);
         for (int i = 0; i < kMaxSlots; ++i) {
-            mbar_init(bars.slot_full(i), kGatherWarps);
+            mbar_init(bars.slot_full(i), 32 * kGatherWarps);
             mbar_init(bars.slot_empty(i), 1);
         }
         T->abort_flag = 0;
@@ -945,8 +983,6 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(
             T->first_tile = t - T->first * P.tiles;
             T->end = share(total, gridDim.x, blockIdx.x + 1);
         }
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_codes)) : "memory");
-        if (P.has_rope) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_rope)) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     // the join may be launched now; it waits for this grid's end
@@ -965,7 +1001,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(
     } else if (warp < R::kGather0) {
         prep_role<N>(P, smem, T, bars);
     } else if (warp < R::kSched) {
-        gather_role<N>(P, &tm_codes, &tm_rope, smem, T, bars);
+        gather_role<N>(P, smem, T, bars);
     } else if (warp == R::kSched) {
         scheduler_role(P, T, bars);
     } else if (warp == R::kQk) {
@@ -1052,19 +1088,6 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __g
     }
 }
 
-// [rows][cols] map for tile::gather4: a box of 128 bytes of one row, 128-byte swizzle.
-bool make_row_map(CUtensorMap *m, const void *ptr, CUtensorMapDataType type, int elem, uint64_t rows, uint64_t cols) {
-    auto fn = encode_fn();
-    if (!fn || rows == 0) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)cols * elem};
-    cuuint32_t box[2] = {(cuuint32_t)(128 / elem), 1u};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(m, type, 2, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Lets a kernel use kSmemBytes of shared memory, once per kernel and device.
 template <auto kKernel> cudaError_t allow_smem() {
     static std::atomic<uint64_t> done{0};               // bit per device below 64
@@ -1078,11 +1101,10 @@ template <auto kKernel> cudaError_t allow_smem() {
 }
 
 template <int N, bool kStats>
-cudaError_t launch_main(const CUtensorMap &tm_codes, const CUtensorMap &tm_rope, const Params &P, int grid,
-                        cudaStream_t st) {
+cudaError_t launch_main(const Params &P, int grid, cudaStream_t st) {
     cudaError_t e = allow_smem<cache_attn_kernel<N, kStats>>();
     if (e != cudaSuccess) return e;
-    cache_attn_kernel<N, kStats><<<grid, Roles<N>::kThreads, kSmemBytes, st>>>(tm_codes, tm_rope, P);
+    cache_attn_kernel<N, kStats><<<grid, Roles<N>::kThreads, kSmemBytes, st>>>(P);
     return cudaGetLastError();
 }
 
@@ -1177,18 +1199,11 @@ cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnP
     P.p_off = p.p_off;
     P.slot_off = p.slot_off;
     P.tmem_cols = p.tmem_cols;
-    CUtensorMap tm_codes, tm_rope;
-    if (!make_row_map(&tm_codes, a.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, P.key_rows, a.Dm)) return cudaErrorInvalidValue;
-    if (a.Dr > 0) {
-        if (!make_row_map(&tm_rope, a.k_rope, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, P.key_rows, 64)) return cudaErrorInvalidValue;
-    } else {
-        tm_rope = tm_codes;
-    }
     // the statistics cost a maximum per score: a kernel of their own
-    cudaError_t e = p.N == 16 ? (smax ? launch_main<16, true>(tm_codes, tm_rope, P, p.grid, st)
-                                      : launch_main<16, false>(tm_codes, tm_rope, P, p.grid, st))
-                              : (smax ? launch_main<32, true>(tm_codes, tm_rope, P, p.grid, st)
-                                      : launch_main<32, false>(tm_codes, tm_rope, P, p.grid, st));
+    cudaError_t e = p.N == 16 ? (smax ? launch_main<16, true>(P, p.grid, st)
+                                      : launch_main<16, false>(P, p.grid, st))
+                              : (smax ? launch_main<32, true>(P, p.grid, st)
+                                      : launch_main<32, false>(P, p.grid, st));
     if (e != cudaSuccess || !p.split) return e;
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
