@@ -25,11 +25,12 @@
 //             before the reference moves; a vote per tile finds that out, and only then are the
 //             maxima reduced and O rescaled. Weights below 2^-18 of the largest may round to 0
 //   prep      the next unit's q: normalised, split and stored in the MMA layout
-//   gather    looks up each selected key's cache row, keeps its scale for the softmax warps and
-//             copies codes and rope part with cp.async into 16 KB slots (128 keys x 128 bytes,
+//   lookup    each selected key's cache row for the gather and its scale for the softmax warps, a few
+//             tiles ahead, and how many tiles a unit has
+//   gather    copies codes and rope part with cp.async into 16 KB slots (128 keys x 128 bytes,
 //             128-byte swizzle); rows that select nothing are zero-filled. TMA's gather of four rows
 //             took %TMA%
-//   scheduler the CTA's units;  qk / pv: one thread each issues the two products
+//   qk, pv    one thread each issues the two products
 // Every wait is bounded in time; on expiry the kernel records LI_DEVERR_TIMEOUT and returns. The
 // softmax warps of a group agree on giving up (the vote carries it), so none is left at a barrier.
 #include <atomic>
@@ -50,7 +51,7 @@ using namespace sm100;
 
 constexpr int kKeys = 128;                          // selected keys per tile (MMA M)
 constexpr uint32_t kSlot = kKeys * 128;             // 128 bytes of 128 keys
-constexpr int kMaxSlots = 16, kTileRing = 8, kAhRing = 4;
+constexpr int kMaxSlots = 16, kTileRing = 4, kAhRing = 4;
 constexpr int kGatherWarps = 4;
 constexpr uint32_t kSmemBytes = 232448;
 constexpr uint32_t kTailBytes = 8192;
@@ -69,12 +70,12 @@ template <int N> struct Roles {
     static constexpr int kSoft = 8;                     // two groups of 4 warps
     static constexpr int kPrep0 = kSoft, kPrep = 4;
     static constexpr int kGather0 = kPrep0 + kPrep;
-    static constexpr int kSched = kGather0 + kGatherWarps, kQk = kSched + 1;    // then pv
-    static constexpr int kThreads = 32 * (kSched + 3);
+    static constexpr int kLookup = kGather0 + kGatherWarps, kQk = kLookup + 1;    // then pv
+    static constexpr int kThreads = 32 * (kLookup + 3);
 };
 
 // What a CTA works on in turn. Every role finds its units by itself (unit_at); only the tiles that
-// are left once those behind the last selected entry are dropped come from the scheduler.
+// are left once those behind the last selected entry are dropped come from the lookup warp.
 struct Unit {
     int32_t row;            // -1: no more units
     int32_t head0;          // first head
@@ -95,11 +96,13 @@ struct Bars {
     __device__ uint32_t p_full(int i) const { return at(12 + i); }
     __device__ uint32_t p_empty(int i) const { return at(14 + i); }
     __device__ uint32_t o_empty() const { return at(16); }
-    __device__ uint32_t meta_full(int i) const { return at(17 + i); }
-    __device__ uint32_t slot_full(int i) const { return at(17 + kTileRing + i); }
-    __device__ uint32_t slot_empty(int i) const { return at(17 + kTileRing + kMaxSlots + i); }
+    __device__ uint32_t rows_full(int i) const { return at(17 + i); }           // a tile's cache rows,
+    __device__ uint32_t scales_full(int i) const { return at(17 + kTileRing + i); }     // its scales,
+    __device__ uint32_t looked_up(int i) const { return at(17 + 2 * kTileRing + i); }   // both read
+    __device__ uint32_t slot_full(int i) const { return at(17 + 3 * kTileRing + i); }
+    __device__ uint32_t slot_empty(int i) const { return at(17 + 3 * kTileRing + kMaxSlots + i); }
 };
-constexpr int kNumBars = 17 + kTileRing + 2 * kMaxSlots;
+constexpr int kNumBars = 17 + 3 * kTileRing + 2 * kMaxSlots;
 struct Tail {
     uint64_t bars[kNumBars];
     int32_t tiles[2];                           // the units' tiles left
@@ -114,6 +117,7 @@ struct Tail {
     alignas(16) float red[2][16][4];            // [group][head][warp]
     alignas(16) float lsum[2][16][4], mx[2][16][4];
     alignas(16) float descale[kTileRing][kKeys];    // kNoKey: the entry selects nothing
+    alignas(16) int32_t row[kTileRing][kKeys];  // cache rows, -1: none; key 32 w + s + 4 i at 32 w + 8 s + i
 };
 static_assert(sizeof(Tail) <= kTailBytes, "shared memory tail");
 
@@ -140,6 +144,10 @@ struct Params {
 struct Ring {
     int idx = 0;
     uint32_t phase = 0;
+    __device__ __forceinline__ void next(int n, int by) {       // by <= n
+        idx += by;
+        if (idx >= n) { idx -= n; phase ^= 1u; }
+    }
     __device__ __forceinline__ void next(int n) {
         if (++idx == n) { idx = 0; phase ^= 1u; }
     }
@@ -283,17 +291,39 @@ __device__ __forceinline__ Unit unit_at(const Params &P, const Tail *T, int it) 
     return u;
 }
 
-// ---- scheduler -----------------------------------------------------------------------------------
-__device__ void scheduler_role(const Params &P, Tail *T, const Bars &bars) {
+// ---- lookups -----------------------------------------------------------------------------------------
+// 4-byte copy into shared memory, tracked like every cp.async of the thread.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// One warp: the tiles of each unit (those behind its last selected entry are left out), and for each
+// tile the cache rows of its keys, four a lane, with their scales on the way into shared memory.
+__device__ void lookup_role(const Params &P, Tail *T, const Bars &bars) {
     const int lane = threadIdx.x & 31;
-    for (int it = 0;; ++it) {
+    Ring tr;
+    uint32_t err = 0;
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
         const Unit u = unit_at(P, T, it);
-        if (u.row < 0) return;
-        // tiles behind the last selected entry are left out
+        if (u.row < 0) break;
         const int32_t *ir = P.indices + (int64_t)u.row * P.topk;
+        const int32_t b = P.by_s1.div(u.row);
+        const int32_t *table = P.block_table ? P.block_table + b * P.bt_stride : nullptr;
         const int from = u.tile0 * kKeys, to = min((u.tile0 + u.tiles) * kKeys, P.topk);
+        const int32_t tail = __ldg(ir + to - 1);
+        int32_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = from + lane + 32 * i;
+            v[i] = p < to ? __ldg(ir + p) : -1;
+        }
+        // the rest of the unit's entries, and the start of its block-table row, on their way to L2
+        for (int p = from + kKeys + 32 * lane; p < to; p += 32 * 32) prefetch_l2(ir + p);
+        if (table && 32 * lane < P.bt_stride) prefetch_l2(table + 32 * lane);
         int tiles = u.tiles;
-        if (__ldg(ir + to - 1) < 0) {
+        if (tail < 0) {
             int last = -1;
 #pragma unroll 8
             for (int p = from + lane; p < to; p += 32)
@@ -301,16 +331,52 @@ __device__ void scheduler_role(const Params &P, Tail *T, const Bars &bars) {
             last = __reduce_max_sync(0xffffffffu, last);
             tiles = last < from ? 0 : (last - from) / kKeys + 1;
         }
-        if (!wait_warp(bars.u_empty(it & 1), ((it >> 1) & 1) ^ 1, &T->abort_flag)) {
-            T->abort_flag = 1;
-            return;
-        }
+        ok = wait_warp(bars.u_empty(it & 1), ((it >> 1) & 1) ^ 1, &T->abort_flag);
+        if (!ok) break;
         if (lane == 0) {
             T->tiles[it & 1] = tiles;
             mbar_arrive(bars.u_full(it & 1));
         }
         __syncwarp();
+        for (int j = 0; j < tiles; ++j, tr.next(kTileRing)) {
+            // positions outside the sequence, blocks outside the cache and negative entries select nothing
+            // (dense keys: one block of S2 rows a batch, batch b's is block b)
+            int32_t blk[4], off[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool in = (uint32_t)v[i] < (uint32_t)P.s2;
+                if (!in && v[i] >= 0) err |= LI_DEVERR_LENGTHS;
+                const int32_t q = table && in ? P.by_block.div(v[i]) : 0;
+                off[i] = in ? v[i] - q * P.block_size : -1;
+                blk[i] = table && in ? __ldg(table + q) : b;
+            }
+            // the next tile's entries
+            const int next = from + (j + 1) * kKeys + lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = next + 32 * i < to ? __ldg(ir + next + 32 * i) : -1;
+            ok = wait_warp(bars.looked_up(tr.idx), tr.phase ^ 1u, &T->abort_flag);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                int32_t r = -1;
+                if (off[i] >= 0) {
+                    if ((uint32_t)blk[i] < (uint32_t)P.num_blocks) r = blk[i] * P.block_size + off[i];
+                    else err |= LI_DEVERR_TABLE;
+                }
+                if (r >= 0 && !idx_ok(r, P.key_rows, P.status)) r = -1;
+                T->row[tr.idx][32 * i + 8 * (lane & 3) + (lane >> 2)] = r;
+                // the scale goes to the softmax warps, which check it
+                float *d = &T->descale[tr.idx][32 * i + lane];
+                if (r >= 0) cp_async4(smem_u32(d), P.descale + r);
+                else *d = __uint_as_float(kNoKey);
+            }
+            mbar_arrive(bars.rows_full(tr.idx));
+            cp_async_arrive(bars.scales_full(tr.idx));
+        }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");    // no copy may outlive the CTA
+    if (!ok) T->abort_flag = 1;
+    if (err && P.status) atomicOr(P.status, err);
 }
 
 // The tiles left of this CTA's it-th unit, for a whole warp; -1 on giving up.
@@ -415,106 +481,52 @@ __device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &b
 }
 
 // ---- gather ----------------------------------------------------------------------------------------
-// The three dependent reads behind a selected key, one function each so that the loop can issue
-// them a tile apart: its position, the block that holds it, its cache row's scale.
-__device__ __forceinline__ int32_t entry_at(const Params &P, const int32_t *ir, int pos, int end) {
-    return pos < end ? __ldg(ir + pos) : -1;
-}
-__device__ __forceinline__ int32_t block_of(const Params &P, int64_t b, int32_t v) {
-    return P.block_table && v >= 0 && v < P.s2 ? __ldg(P.block_table + b * P.bt_stride + P.by_block.div(v)) : 0;
-}
-// Cache row of position v, -1 where it selects nothing.
-__device__ __forceinline__ int32_t row_of(const Params &P, int64_t b, int32_t v, int32_t blk, uint32_t *err) {
-    if (v < 0) return -1;
-    if (v >= P.s2) {
-        *err |= LI_DEVERR_LENGTHS;
-        return -1;
-    }
-    if (!P.block_table) return (int32_t)(b * P.s2 + v);
-    if (blk < 0 || blk >= P.num_blocks) {
-        *err |= LI_DEVERR_TABLE;
-        return -1;
-    }
-    return blk * P.block_size + v - P.by_block.div(v) * P.block_size;
-}
-
-// 4-byte copy into shared memory, tracked like every cp.async of the thread.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-
 template <int N>
 __device__ void gather_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bars) {
     const int w = (threadIdx.x >> 5) - Roles<N>::kGather0, lane = threadIdx.x & 31;
     const int piece = lane & 7, sub = lane >> 3;        // this lane copies keys 32 w + sub + 4 i
+    const uint8_t *codes = P.codes + piece * 16, *ropes = reinterpret_cast<const uint8_t *>(P.k_rope) + piece * 16;
     // 16-byte piece of row key in a swizzled slot; key & 7 is sub + 4 (i & 1)
     const uint32_t dst = smem_u32(smem) + P.slot_off + (32 * w + sub) * 128;
     const uint32_t even = (uint32_t)((piece ^ sub) << 4), odd = (uint32_t)((piece ^ (sub + 4)) << 4);
     Ring sr, tr;
-    uint32_t err = 0;
     bool ok = true;
     for (int it = 0; ok; ++it) {
-        // the first lookups do not wait for the scheduler
-        const Unit u = unit_at(P, T, it);
-        if (u.row < 0) break;
-        const int32_t *ir = P.indices + (int64_t)u.row * P.topk;
-        const int64_t b = P.by_s1.div(u.row);
-        int pos = u.tile0 * kKeys + 32 * w + lane;
-        const int end = min((u.tile0 + u.tiles) * kKeys, P.topk);
-        int32_t va = entry_at(P, ir, pos, end), vb = entry_at(P, ir, pos + kKeys, end);
-        int32_t vc = entry_at(P, ir, pos + 2 * kKeys, end);
-        const int32_t blk0 = block_of(P, b, va);
-        int32_t blk_a = 0, blk_b = block_of(P, b, vb);
-        int32_t mine = row_of(P, b, va, blk0, &err);
-        va = vc;
+        if (unit_at(P, T, it).row < 0) break;
         const int tiles = take_tiles(T, bars, it);
-        if (tiles < 0) { ok = false; break; }
-        // One tile: its copies, then the lookups of the next (whose position and block are in v1 and
-        // blk1) and of the one after (position in v2); v1 takes the position of the third. Two tiles a
-        // turn with the registers' parts exchanged: a move of one still being read would wait for it.
-        const auto tile = [&](int32_t &v1, int32_t &blk1, int32_t &v2, int32_t &blk2) {
-            if (mine >= 0 && !idx_ok(mine, P.key_rows, P.status)) mine = -1;
-            // the key's scale for the softmax warps, checked there
-            float *d = &T->descale[tr.idx][32 * w + lane];
-            if (mine >= 0) {
-                cp_async4(smem_u32(d), P.descale + mine);
-                cp_async_arrive(bars.meta_full(tr.idx));
-            } else {
-                *d = __uint_as_float(kNoKey);
-                mbar_arrive(bars.meta_full(tr.idx));
-            }
+        ok = tiles >= 0;
+        for (int j = 0; j < tiles && ok; ++j, tr.next(kTileRing)) {
+            ok = wait_warp(bars.rows_full(tr.idx), tr.phase, &T->abort_flag);
+            if (!ok) break;
+            // the eight rows of this lane, and 16 bytes of each piece or none
+            int32_t r[8];
+            *reinterpret_cast<int4 *>(r) = *reinterpret_cast<const int4 *>(&T->row[tr.idx][32 * w + 8 * sub]);
+            *reinterpret_cast<int4 *>(r + 4) = *reinterpret_cast<const int4 *>(&T->row[tr.idx][32 * w + 8 * sub + 4]);
             __syncwarp();
-            // the eight rows of this lane: where they start, and 16 bytes of each piece or none
+            if (lane == 0) mbar_arrive(bars.looked_up(tr.idx));
             const uint8_t *row[8];
             uint32_t size[8];
             bool there = true;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int32_t r = __shfl_sync(0xffffffffu, mine, sub + 4 * i);
-                size[i] = r < 0 ? 0u : 16u;
-                row[i] = P.codes + (int64_t)max(r, 0) * P.Dm + piece * 16;
+                size[i] = r[i] < 0 ? 0u : 16u;
+                r[i] = max(r[i], 0);
+                row[i] = codes + (uint64_t)(uint32_t)r[i] * (uint32_t)P.Dm;
             }
             if (P.has_rope) {
-                const uint8_t *rope[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int32_t r = __shfl_sync(0xffffffffu, mine, sub + 4 * i);
-                    rope[i] = reinterpret_cast<const uint8_t *>(P.k_rope) + (int64_t)max(r, 0) * 128 + piece * 16;
-                }
                 there = wait_lane(bars.slot_empty(sr.idx), sr.phase ^ 1u, &T->abort_flag);
                 if (there) {
                     const uint32_t to = dst + sr.idx * kSlot;
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        cp_async16_zfill(to + i * 512 + (i & 1 ? odd : even), rope[i], size[i]);
+                        cp_async16_zfill(to + i * 512 + (i & 1 ? odd : even), ropes + (uint64_t)(uint32_t)r[i] * 128u, size[i]);
                     cp_async_arrive(bars.slot_full(sr.idx));
                 }
                 sr.next(P.slots);
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                if (c >= P.blocks) break;
-                if (!there) break;              // a slot that is not free is not written
+                if (c >= P.blocks || !there) break;     // a slot that is not free is not written
                 there = wait_lane(bars.slot_empty(sr.idx), sr.phase ^ 1u, &T->abort_flag);
                 if (!there) break;
                 const uint32_t to = dst + sr.idx * kSlot;
@@ -524,23 +536,11 @@ __device__ void gather_role(const Params &P, uint8_t *smem, Tail *T, const Bars 
                 cp_async_arrive(bars.slot_full(sr.idx));
                 sr.next(P.slots);
             }
-            if (!__all_sync(0xffffffffu, there)) return false;
-            tr.next(kTileRing);
-            pos += kKeys;
-            mine = row_of(P, b, v1, blk1, &err);
-            blk2 = block_of(P, b, v2);
-            v1 = entry_at(P, ir, pos + 2 * kKeys, end);
-            return true;
-        };
-        for (int j = 0; j < tiles && ok; j += 2) {
-            ok = tile(vb, blk_b, va, blk_a);
-            if (ok && j + 1 < tiles) ok = tile(va, blk_a, vb, blk_b);
+            ok = __all_sync(0xffffffffu, there);
         }
     }
-    // no copy may still be writing shared memory when the CTA leaves
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    asm volatile("cp.async.wait_all;" ::: "memory");    // no copy may outlive the CTA
     if (!ok) T->abort_flag = 1;
-    if (err && P.status) atomicOr(P.status, err);
 }
 
 // ---- products --------------------------------------------------------------------------------------
@@ -602,7 +602,7 @@ __device__ void qk_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
                 if (ok) umma_commit(bars.s_full(b));
             }
             ok = __all_sync(0xffffffffu, ok);
-            for (int c = P.has_rope ? -1 : 0; c < P.blocks; ++c) sr.next(P.slots);
+            sr.next(P.slots, P.has_rope + P.blocks);
         }
         if (!ok) break;
         if (elect_one()) umma_commit(bars.q_empty(qr.idx));
@@ -632,10 +632,10 @@ __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
             fence_async_smem();                 // the weights, for the async proxy
             tc_fence_after();
             const uint64_t p = weights_desc<N>(sbase + P.p_off + (kt & 1u) * (2 * N * 128));
-            if (P.has_rope) sr.next(P.slots);
             // one elected lane for the whole tile
             if (elect_one()) {
-                int slot = sr.idx;
+                int slot = sr.idx + P.has_rope;
+                if (slot == P.slots) slot = 0;
 #pragma unroll 4
                 for (int c = 0; c < P.blocks; ++c) {
                     const uint64_t v = sw128_desc_mn(slots + slot * kSlot, kSlot);
@@ -649,7 +649,7 @@ __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
                 umma_commit(bars.p_empty(kt & 1u));
             }
             __syncwarp();
-            for (int c = 0; c < P.blocks; ++c) sr.next(P.slots);
+            sr.next(P.slots, P.has_rope + P.blocks);
         }
         if (!ok) break;
         ++nu;
@@ -714,7 +714,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
         const float *ref = T->ref[g];
         for (int j = 0; j < tiles; ++j, ++kt, tr.next(kTileRing)) {
             const uint32_t b = kt & 1u;
-            ok = ok && wait_lane(bars.meta_full(tr.idx), tr.phase, abort_flag);
+            ok = ok && wait_lane(bars.scales_full(tr.idx), tr.phase, abort_flag);
             // an entry that selects nothing, or whose scale is out of range, has scale 0 and a weight
             // of 2^-inf
             float d = ok ? T->descale[tr.idx][key] : 0.0f;
@@ -722,6 +722,8 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 bad |= ok && __float_as_uint(d) != kNoKey;
                 d = 0.0f;
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.looked_up(tr.idx));
             const float log2d = log2f(d), inv_d = d > 0.0f ? __frcp_rn(d) : 0.0f;
             ok = ok && wait_lane(bars.s_full(b), (kt >> 1) & 1u, abort_flag);
             float t[H];                                 // y - ref, the weights' exponents
@@ -971,7 +973,11 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const
             mbar_init(bars.p_empty(i), 1);
         }
         mbar_init(bars.o_empty(), R::kSoft);
-        for (int i = 0; i < kTileRing; ++i) mbar_init(bars.meta_full(i), 32 * kGatherWarps);
+        for (int i = 0; i < kTileRing; ++i) {
+            mbar_init(bars.rows_full(i), 32);
+            mbar_init(bars.scales_full(i), 32);
+            mbar_init(bars.looked_up(i), kGatherWarps + R::kSoft);
+        }
         for (int i = 0; i < kMaxSlots; ++i) {
             mbar_init(bars.slot_full(i), 32 * kGatherWarps);
             mbar_init(bars.slot_empty(i), 1);
@@ -1000,10 +1006,10 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const
         softmax_role<N, kStats>(P, smem, T, bars, tmem);
     } else if (warp < R::kGather0) {
         prep_role<N>(P, smem, T, bars);
-    } else if (warp < R::kSched) {
+    } else if (warp < R::kLookup) {
         gather_role<N>(P, smem, T, bars);
-    } else if (warp == R::kSched) {
-        scheduler_role(P, T, bars);
+    } else if (warp == R::kLookup) {
+        lookup_role(P, T, bars);
     } else if (warp == R::kQk) {
         qk_role<N>(P, smem, T, bars, tmem);
     } else {
@@ -1131,8 +1137,6 @@ bool cache_attn_plan(const li_cache_attn_args &a, CacheAttnPlan *p) {
         if (slot_off >= kTailOff) continue;
         int slots = (int)((kTailOff - slot_off) / kSlot);
         slots = slots < kMaxSlots ? slots : kMaxSlots;
-        // the gather runs at most this many tiles ahead of the softmax (the rings of kTileRing)
-        if (slots > (kTileRing - 2) * per_tile) slots = (kTileRing - 2) * per_tile;
         if (slots < 2 * per_tile) continue;
         p->q_bufs = bufs;
         p->p_off = off;
@@ -1176,6 +1180,8 @@ cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnP
         P.num_blocks = a.num_blocks;
         P.key_rows = (int64_t)a.num_blocks * a.block_size;
     } else {
+        P.block_size = a.s2;
+        P.num_blocks = a.batch;
         P.key_rows = (int64_t)a.batch * a.s2;
     }
     P.units = p.units;
