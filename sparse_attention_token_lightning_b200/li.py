@@ -650,14 +650,28 @@ def rope_grad(dy, positions, freqs: RopeFrequencies, offset: int = 0, interleave
     return _rope(lib().li_rope_grad, dy, positions, freqs, offset, interleaved, out, stream)
 
 
-def _no_head(t, dims, name):
-    """(..., 1, D) seen as (..., D): keys have one head."""
-    n = t.dim()
-    if n == dims:
-        return t
-    if n != dims + 1 or t.shape[-2] != 1:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, {dims} dimensions (or a head of 1 more) wanted")
-    return t.squeeze(-2)
+def _rows_of(t, dims, name):
+    """Shape and strides of rows (..., D) in `dims` dimensions, a head dimension of 1 before D
+    left out: keys have one head."""
+    shape, strides = t.shape, t.stride()
+    n = len(shape)
+    if n == dims + 1 and shape[-2] == 1:
+        shape, strides = shape[:-2] + shape[-1:], strides[:-2] + strides[-1:]
+    elif n != dims:
+        raise ValueError(f"{name} has shape {tuple(shape)}, {dims} dimensions (or a head of 1 more) wanted")
+    if shape[-1] > 1 and strides[-1] != 1:
+        raise ValueError(f"the last dimension of {name} must be dense")
+    return shape, strides
+
+
+def _cache_ptr(t, dev, name, dtype, n0, n1, D):
+    """Address of a contiguous cache (n0, n1, 1, D) or (n0, n1, D)."""
+    shape = t.shape
+    if (t.device != dev or t.dtype is not dtype or not t.is_contiguous() or
+            (shape != (n0, n1, 1, D) and shape != (n0, n1, D))):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {(n0, n1, 1, D)} on {dev}, got "
+                         f"{t.dtype} {tuple(shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr()
 
 
 def make_cache_args(x, codes, descale, rope=None, rope_cache=None, seqused_k=None,
@@ -671,11 +685,8 @@ def make_cache_args(x, codes, descale, rope=None, rope_cache=None, seqused_k=Non
     a = LiCacheArgs()
     tnd = cu_seqlens is not None
     dims = 2 if tnd else 3
-    x, codes = _no_head(x, dims, "x"), _no_head(codes, 3, "codes")
-    shape, strides = x.shape, x.stride()
-    D, (n0, n1, _) = shape[-1], codes.shape
-    if D > 1 and strides[-1] != 1:
-        raise ValueError("the last dimension of x must be dense")
+    shape, strides = _rows_of(x, dims, "x")
+    D, (n0, n1) = shape[-1], codes.shape[:2]
     a.x, a.x_row_stride = x.data_ptr(), strides[-2]
     if tnd:
         B = cu_seqlens.shape[0] - 1
@@ -685,7 +696,7 @@ def make_cache_args(x, codes, descale, rope=None, rope_cache=None, seqused_k=Non
         B = shape[0]
         a.x_len, a.x_batch_stride = shape[1], strides[0]
     a.batch, a.dim, a.dtype = B, D, dtype
-    a.codes = _ptr_of(codes, dev, "codes", torch.float8_e4m3fn, (n0, n1, D))
+    a.codes = _cache_ptr(codes, dev, "codes", torch.float8_e4m3fn, n0, n1, D)
     a.descale = _ptr_of(descale, dev, "descale", torch.float32, (n0, n1))
     if pow2:
         a.pow2 = 1
@@ -705,15 +716,15 @@ def make_cache_args(x, codes, descale, rope=None, rope_cache=None, seqused_k=Non
     if (rope is None) != (rope_cache is None):
         raise ValueError("rope and rope_cache go together")
     if rope is not None:
-        rope = _no_head(rope, dims, "rope")
-        R, strides = rope.shape[-1], rope.stride()
-        if rope.device != dev or rope.dtype is not kind or rope.shape[:-1] != shape[:-1] or (R > 1 and strides[-1] != 1):
-            raise ValueError(f"rope must be {kind} {tuple(shape[:-1])} + (rope_dim,) on {dev}, its last "
-                             f"dimension dense, got {rope.dtype} {tuple(rope.shape)} on {rope.device}")
+        rows, strides = _rows_of(rope, dims, "rope")
+        R = rows[-1]
+        if rope.device != dev or rope.dtype is not kind or rows[:-1] != shape[:-1]:
+            raise ValueError(f"rope must be {kind} {tuple(shape[:-1])} + (rope_dim,) on {dev}, got "
+                             f"{rope.dtype} {tuple(rope.shape)} on {rope.device}")
         a.rope, a.rope_row_stride, a.rope_dim = rope.data_ptr(), strides[-2], R
         if not tnd:
             a.rope_batch_stride = strides[0]
-        a.rope_cache = _ptr_of(_no_head(rope_cache, 3, "rope_cache"), dev, "rope_cache", kind, (n0, n1, R))
+        a.rope_cache = _cache_ptr(rope_cache, dev, "rope_cache", kind, n0, n1, R)
     if device_status is not None:
         a.device_status = _status_ptr(device_status, dev)
     return a
@@ -784,9 +795,8 @@ def make_cache_attn_args(q, codes, descale, sparse_indices, scale, q_rope=None, 
     B, S1, G, Dm = shape = q.shape
     a = LiCacheAttnArgs()
     a.q = _ptr_of(q, dev, "q", torch.bfloat16, shape)
-    codes = _no_head(codes, 3, "codes")
-    n0, n1, _ = codes.shape
-    a.codes = _ptr_of(codes, dev, "codes", torch.float8_e4m3fn, (n0, n1, Dm))
+    n0, n1 = codes.shape[:2]
+    a.codes = _cache_ptr(codes, dev, "codes", torch.float8_e4m3fn, n0, n1, Dm)
     a.descale = _ptr_of(descale, dev, "descale", torch.float32, (n0, n1))
     topk = sparse_indices.shape[-1]
     a.sparse_indices = _ptr_of(sparse_indices, dev, "sparse_indices", torch.int32, (B, S1, 1, topk))
@@ -796,7 +806,7 @@ def make_cache_attn_args(q, codes, descale, sparse_indices, scale, q_rope=None, 
     if q_rope is not None:
         R = q_rope.shape[-1]
         a.q_rope = _ptr_of(q_rope, dev, "q_rope", torch.bfloat16, (B, S1, G, R))
-        a.k_rope = _ptr_of(_no_head(rope_cache, 3, "rope_cache"), dev, "rope_cache", torch.bfloat16, (n0, n1, R))
+        a.k_rope = _cache_ptr(rope_cache, dev, "rope_cache", torch.bfloat16, n0, n1, R)
         a.Dr = R
     if block_table is not None:
         width = block_table.shape[-1]
