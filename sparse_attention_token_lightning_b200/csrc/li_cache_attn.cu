@@ -17,9 +17,9 @@
 // the key tile read MN-major, keys on K) both read the same gathered tile; the rope part is a bf16
 // product of its own into other TMEM columns, since its codes have no scale.
 //
-// One CTA per SM works on units (row, block of up to 32 heads), whole units in turn when there are
-// many rows, or an equal share of all units' tiles of 128 selected keys when there are few
-// (decode): a unit cut between CTAs leaves partial outputs, which a second kernel joins. Warps:
+// One CTA per SM works in turn on units: a row, a block of up to 32 heads, and all tiles of 128 selected
+// keys or, when there are few rows (decode), one of several equal pieces of them; pieces leave partial
+// outputs, which a second kernel joins (cache_attn_plan says when). Warps:
 //   softmax   two groups of 4 warps, each with half the heads: a thread owns one key of the tile and
 //             8 or 16 heads. The largest weight is set to 2^4 and may grow to 2^8 (E4M3 holds 448)
 //             before the reference moves; a vote per tile finds that out, and only then are the
@@ -29,7 +29,8 @@
 //             tiles ahead, and how many tiles a unit has
 //   gather    copies codes and rope part with cp.async into 16 KB slots (128 keys x 128 bytes,
 //             128-byte swizzle); rows that select nothing are zero-filled. TMA's gather of four rows
-//             took %TMA%
+//             takes as long (attention of 64 single tokens 30.2 us against 30.9, one token 13.2 against
+//             12.8, 2048 tokens 205 against 204) and wants tensor maps from the host
 //   qk, pv    one thread each issues the two products
 // Every wait is bounded in time; on expiry the kernel records LI_DEVERR_TIMEOUT and returns. The
 // softmax warps of a group agree on giving up (the vote carries it), so none is left at a barrier.
@@ -66,11 +67,11 @@ constexpr float kMinDescale = 7.888609052210118e-31f, kMaxDescale = 1.2676506002
 constexpr uint32_t kDevErrInternal = 0x20u;
 
 template <int N> struct Roles {
-    static constexpr int kHeads = N / 2;                // heads of a softmax thread
-    static constexpr int kSoft = 8;                     // two groups of 4 warps
+    static constexpr int kHeads = N / 2;                // heads of a softmax group (4 warps) and thread
+    static constexpr int kSoft = 8;
     static constexpr int kPrep0 = kSoft, kPrep = 4;
     static constexpr int kGather0 = kPrep0 + kPrep;
-    static constexpr int kLookup = kGather0 + kGatherWarps, kQk = kLookup + 1;    // then pv
+    static constexpr int kLookup = kGather0 + kGatherWarps, kQk = kLookup + 1;  // then pv
     static constexpr int kThreads = 32 * (kLookup + 3);
 };
 
@@ -80,7 +81,7 @@ struct Unit {
     int32_t row;            // -1: no more units
     int32_t head0;          // first head
     int32_t tile0, tiles;   // tiles of the row's selection
-    int32_t part;           // partial slot, or -1: the unit is whole
+    int32_t part;           // partial slot, or -1: the unit has the whole selection
 };
 
 // Barriers and small arrays in the shared-memory tail.
@@ -89,29 +90,29 @@ struct Bars {
     __device__ uint32_t at(int i) const { return base + 8 * i; }
     __device__ uint32_t u_full(int i) const { return at(0 + i); }
     __device__ uint32_t u_empty(int i) const { return at(2 + i); }
-    __device__ uint32_t q_full(int i) const { return at(4 + i); }
-    __device__ uint32_t q_empty(int i) const { return at(6 + i); }
-    __device__ uint32_t s_full(int i) const { return at(8 + i); }
-    __device__ uint32_t s_empty(int i) const { return at(10 + i); }
-    __device__ uint32_t p_full(int i) const { return at(12 + i); }
-    __device__ uint32_t p_empty(int i) const { return at(14 + i); }
-    __device__ uint32_t o_empty() const { return at(16); }
-    __device__ uint32_t rows_full(int i) const { return at(17 + i); }           // a tile's cache rows,
-    __device__ uint32_t scales_full(int i) const { return at(17 + kTileRing + i); }     // its scales,
-    __device__ uint32_t looked_up(int i) const { return at(17 + 2 * kTileRing + i); }   // both read
-    __device__ uint32_t slot_full(int i) const { return at(17 + 3 * kTileRing + i); }
-    __device__ uint32_t slot_empty(int i) const { return at(17 + 3 * kTileRing + kMaxSlots + i); }
+    __device__ uint32_t q_full() const { return at(4); }
+    __device__ uint32_t q_empty() const { return at(5); }
+    __device__ uint32_t s_full(int i) const { return at(6 + i); }
+    __device__ uint32_t s_empty(int i) const { return at(8 + i); }
+    __device__ uint32_t p_full(int i) const { return at(10 + i); }
+    __device__ uint32_t p_empty(int i) const { return at(12 + i); }
+    __device__ uint32_t o_empty() const { return at(14); }
+    __device__ uint32_t rows_full(int i) const { return at(15 + i); }           // a tile's cache rows,
+    __device__ uint32_t scales_full(int i) const { return at(15 + kTileRing + i); }     // its scales,
+    __device__ uint32_t looked_up(int i) const { return at(15 + 2 * kTileRing + i); }   // both read
+    __device__ uint32_t slot_full(int i) const { return at(15 + 3 * kTileRing + i); }
+    __device__ uint32_t slot_empty(int i) const { return at(15 + 3 * kTileRing + kMaxSlots + i); }
 };
-constexpr int kNumBars = 17 + 3 * kTileRing + 2 * kMaxSlots;
+constexpr int kNumBars = 15 + 3 * kTileRing + 2 * kMaxSlots;
 struct Tail {
     uint64_t bars[kNumBars];
     int32_t tiles[2];                           // the units' tiles left
-    uint32_t first, first_tile, end;            // split: first unit and its first tile, end of the share
     uint32_t tmem;
     volatile int abort_flag;
-    alignas(16) int vote[2][2][4];              // [group][tile parity][warp]
+    alignas(16) int vote[2][2][4];              // [group][turn][warp]
     alignas(16) float ah[kAhRing][32];          // scale log2(e) / the head's power of two
     alignas(16) float ref[2][16];               // [group][head]: y of a weight 1
+    alignas(16) float coef[2][16];              // what O counts in the output
     alignas(16) float alpha[2][16], moved[2][16];
     int seen[2][16], fresh[2];                  // whether a head's reference is set; any that is not
     alignas(16) float red[2][16][4];            // [group][head][warp]
@@ -130,15 +131,15 @@ struct Params {
     uint32_t *status;
     uint16_t *out;
     float *smax, *ssum;
-    float *part_o, *part_stat;          // [2 grid][N][Dm], [2 grid][N][3]
+    float *part_o, *part_stat;          // [units][N][Dm], [units][N][3]
     int64_t bt_stride, key_rows;
     int64_t units;
     float scale;
     int32_t rows, s1, s2, G, Dm, topk, block_size, num_blocks;
-    int32_t has_rope, blocks, head_blocks, tiles, split;
-    int32_t q_bufs, slots;
-    uint32_t q_bytes, p_off, slot_off, tmem_cols;
-    FixedDiv by_block, by_s1, by_heads;
+    int32_t has_rope, blocks, head_blocks, tiles, cuts, chunk;     // cuts: pieces per selection, of chunk tiles
+    int32_t slots;
+    uint32_t p_off, slot_off, tmem_cols;
+    FixedDiv by_block, by_s1, by_heads, by_cuts;
 };
 
 struct Ring {
@@ -267,27 +268,20 @@ __device__ __forceinline__ float transpose_reduce(const float (&v)[H], int lane)
     return a[0];
 }
 
-// First tile of CTA c's share of all units' tiles (rows are cut only where total x grid is far
-// inside 32 bits).
-__device__ __forceinline__ uint32_t share(uint32_t total, uint32_t grid, uint32_t c) { return total * c / grid; }
-
 // The it-th unit of this CTA.
-__device__ __forceinline__ Unit unit_at(const Params &P, const Tail *T, int it) {
+__device__ __forceinline__ Unit unit_at(const Params &P, int it) {
     Unit u{-1, 0, 0, P.tiles, -1};
-    uint32_t unit;
-    if (P.split) {
-        unit = T->first + it;
-        const uint32_t t = unit * P.tiles;              // the unit's first tile
-        if (t >= T->end) return u;
-        u.tile0 = it == 0 ? (int32_t)T->first_tile : 0;
-        u.tiles = (int32_t)(min((uint32_t)P.tiles, T->end - t) - u.tile0);
-        if (u.tiles != P.tiles) u.part = 2 * blockIdx.x + (u.tile0 == 0 ? 1 : 0);
-    } else {
-        unit = blockIdx.x + (uint32_t)it * gridDim.x;       // units are below 2^26
-        if (unit >= (uint32_t)P.units) return u;
+    const int64_t i = blockIdx.x + (int64_t)it * gridDim.x;
+    if (i >= P.units) return u;                         // below 2^26
+    int32_t whole = (int32_t)i;
+    if (P.cuts > 1) {
+        whole = P.by_cuts.div(whole);
+        u.tile0 = ((int32_t)i - whole * P.cuts) * P.chunk;
+        u.tiles = min(P.chunk, P.tiles - u.tile0);
+        u.part = (int32_t)i;
     }
-    u.row = P.by_heads.div((int32_t)unit);
-    u.head0 = ((int32_t)unit - u.row * P.head_blocks) * 32;
+    u.row = P.by_heads.div(whole);
+    u.head0 = (whole - u.row * P.head_blocks) * 32;
     return u;
 }
 
@@ -306,7 +300,7 @@ __device__ void lookup_role(const Params &P, Tail *T, const Bars &bars) {
     uint32_t err = 0;
     bool ok = true;
     for (int it = 0; ok; ++it) {
-        const Unit u = unit_at(P, T, it);
+        const Unit u = unit_at(P, it);
         if (u.row < 0) break;
         const int32_t *ir = P.indices + (int64_t)u.row * P.topk;
         const int32_t b = P.by_s1.div(u.row);
@@ -394,14 +388,12 @@ __device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &b
     using R = Roles<N>;
     const int wp = (threadIdx.x >> 5) - R::kPrep0, lane = threadIdx.x & 31;
     const float kInf = __int_as_float(0x7f800000);
-    Ring qr;
     int n = 0;                                  // units with tiles so far
     for (int it = 0;; ++it) {
-        const Unit u = unit_at(P, T, it);
+        const Unit u = unit_at(P, it);
         if (u.row < 0) return;
         const int heads = min(P.G - u.head0, N);
         const int64_t row0 = (int64_t)u.row * P.G + u.head0;
-        uint8_t *qb = nullptr;
         bool some = true;
         for (int h0 = wp; h0 < N && some; h0 += 4 * R::kPrep) {
             // four heads of the warp at once, so that their reads overlap; the first four are read
@@ -426,14 +418,13 @@ __device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &b
                 const int tiles = take_tiles(T, bars, it);
                 some = tiles != 0;
                 if (!some) break;
-                if (tiles < 0 || !wait_warp(bars.q_empty(qr.idx), qr.phase ^ 1u, &T->abort_flag)) {
+                if (tiles < 0 || !wait_warp(bars.q_empty(), (n & 1) ^ 1, &T->abort_flag)) {
                     T->abort_flag = 1;
                     return;
                 }
-                qb = smem + qr.idx * P.q_bytes;
             }
             if (P.has_rope)
-                *reinterpret_cast<uint4 *>(qb + P.blocks * (2 * N * 128) + rh * 128 + ((piece ^ (rh & 7)) << 4)) = rope;
+                *reinterpret_cast<uint4 *>(smem + P.blocks * (2 * N * 128) + rh * 128 + ((piece ^ (rh & 7)) << 4)) = rope;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 const int h = h0 + t * R::kPrep;
@@ -465,17 +456,16 @@ __device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &b
                     }
                     const int off = (vec * 8) & 127, b = vec >> 4;
                     const uint32_t at = (uint32_t)(b * 2 * N * 128 + (((off >> 4) ^ (h & 7)) << 4) + (off & 8));
-                    *reinterpret_cast<uint2 *>(qb + at + h * 128) =
+                    *reinterpret_cast<uint2 *>(smem + at + h * 128) =
                         make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-                    *reinterpret_cast<uint2 *>(qb + at + (N + h) * 128) =
+                    *reinterpret_cast<uint2 *>(smem + at + (N + h) * 128) =
                         make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
                 }
             }
         }
         if (!some) continue;                    // a unit without tiles
         fence_async_smem();
-        mbar_arrive(bars.q_full(qr.idx));
-        qr.next(P.q_bufs);
+        mbar_arrive(bars.q_full());
         ++n;
     }
 }
@@ -492,7 +482,7 @@ __device__ void gather_role(const Params &P, uint8_t *smem, Tail *T, const Bars 
     Ring sr, tr;
     bool ok = true;
     for (int it = 0; ok; ++it) {
-        if (unit_at(P, T, it).row < 0) break;
+        if (unit_at(P, it).row < 0) break;
         const int tiles = take_tiles(T, bars, it);
         ok = tiles >= 0;
         for (int j = 0; j < tiles && ok; ++j, tr.next(kTileRing)) {
@@ -554,15 +544,14 @@ __device__ void qk_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
     constexpr uint32_t kQBlock = 2 * N * 128;
     constexpr uint32_t idesc8 = (1u << 4) | ((2u * N >> 3) << 17) | (8u << 24);
     constexpr uint32_t idesc16 = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
-    Ring qr, sr;
-    uint32_t kt = 0;
+    Ring sr;
+    uint32_t kt = 0, nu = 0;
     for (int it = 0;; ++it) {
-        if (unit_at(P, T, it).row < 0) return;
+        if (unit_at(P, it).row < 0) return;
         const int tiles = take_tiles(T, bars, it);
         if (tiles < 0) break;
         if (tiles == 0) continue;
-        if (!wait_warp(bars.q_full(qr.idx), qr.phase, &T->abort_flag)) break;
-        const uint32_t qa = sbase + qr.idx * P.q_bytes;
+        if (!wait_warp(bars.q_full(), nu & 1u, &T->abort_flag)) break;
         bool ok = true;
         for (int j = 0; j < tiles && ok; ++j, ++kt) {
             const uint32_t b = kt & 1u, d = tmem + b * kSCols<N>;
@@ -579,7 +568,7 @@ __device__ void qk_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
                     ok = wait_lane(bars.slot_full(slot), phase, &T->abort_flag);
                     fence_async_smem();         // the gathered rows, for the async proxy
                     tc_fence_after();
-                    const uint64_t a = sw128_desc(slots + slot * kSlot), q = sw128_desc(qa + P.blocks * kQBlock);
+                    const uint64_t a = sw128_desc(slots + slot * kSlot), q = sw128_desc(sbase + P.blocks * kQBlock);
                     if (ok) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) umma_f16(d + 2 * N, a + 2 * k, q + 2 * k, idesc16, k > 0);
@@ -594,7 +583,7 @@ __device__ void qk_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
                     if (!ok) break;
                     fence_async_smem();
                     tc_fence_after();
-                    const uint64_t a = sw128_desc(slots + slot * kSlot), q = sw128_desc(qa + c * kQBlock);
+                    const uint64_t a = sw128_desc(slots + slot * kSlot), q = sw128_desc(sbase + c * kQBlock);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) umma_f8(d, a + 2 * k, q + 2 * k, idesc8, (c | k) != 0);
                     next();
@@ -605,9 +594,9 @@ __device__ void qk_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
             sr.next(P.slots, P.has_rope + P.blocks);
         }
         if (!ok) break;
-        if (elect_one()) umma_commit(bars.q_empty(qr.idx));
+        if (elect_one()) umma_commit(bars.q_empty());
         __syncwarp();
-        qr.next(P.q_bufs);
+        ++nu;
     }
     T->abort_flag = 1;
 }
@@ -619,7 +608,7 @@ __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
     Ring sr;
     uint32_t kt = 0, nu = 0;
     for (int it = 0;; ++it) {
-        if (unit_at(P, T, it).row < 0) return;
+        if (unit_at(P, it).row < 0) return;
         const int tiles = take_tiles(T, bars, it);
         if (tiles < 0) break;
         if (tiles == 0) continue;
@@ -666,84 +655,87 @@ __device__ __forceinline__ void lds4(const float *p, float (&v)[4]) {
 
 template <int N, bool kStats>
 __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bars, uint32_t tmem) {
-    constexpr int H = Roles<N>::kHeads;                 // heads of a thread
+    constexpr int H = Roles<N>::kHeads;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = warp >> 2, q = warp & 3;              // group (H heads), quarter of the TMEM lanes
+    const int g = warp >> 2, q = warp & 3;              // group, quarter of the TMEM lanes
     const int key = 32 * q + lane;                      // key of the tile; dim of an O block
+    const int col = H * g;                              // the group's first head
+    const bool holds = (lane & (32 / H - 1)) == 0;      // the lane has a reduced value, of this head:
+    const int held = lane / (32 / H);
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const float kInf = __int_as_float(0x7f800000);
     volatile int *abort_flag = &T->abort_flag;
     const int bar_id = 1 + g;
     const float rs = P.scale * kLog2e;
-    Ring tr;
     uint32_t kt = 0;
+    uint32_t turn = 0;                                  // votes of the group
     int nu = 0;
     bool ok = true, bad = false;
     for (int it = 0;; ++it) {
-        const Unit u = unit_at(P, T, it);
+        const Unit u = unit_at(P, it);
         if (u.row < 0) {
             if (bad && P.status) atomicOr(P.status, LI_DEVERR_DESCALE);
             return;
         }
-        // the group's warps agree on giving up here too (a vote below carries a failure on)
-        const bool got = wait_warp(bars.u_full(it & 1), (it >> 1) & 1, abort_flag) && ok;
-        if (lane == 0) T->vote[g][kt & 1][q] = got ? 0 : 2;
+        // the group's warps agree on giving up here and by a vote per tile, so that none is left at a
+        // barrier
+        ok = wait_warp(bars.u_full(it & 1), (it >> 1) & 1, abort_flag) && ok;
+        if (lane == 0) T->vote[g][turn & 1][q] = ok ? 0 : 2;
         if (q == 0 && lane < H) {
             T->ref[g][lane] = 0.0f;
             T->seen[g][lane] = 0;
         }
         named_bar(bar_id, 128);
         {
-            const int4 v = *reinterpret_cast<const int4 *>(T->vote[g][kt & 1]);
+            const int4 v = *reinterpret_cast<const int4 *>(T->vote[g][turn++ & 1]);
             if ((v.x | v.y | v.z | v.w) & 2) break;
         }
+        bool failed = false;
         const int tiles = T->tiles[it & 1];
-        named_bar(bar_id, 128);                         // the vote slot is written again below
+        __syncwarp();
         if (lane == 0) mbar_arrive(bars.u_empty(it & 1));
-        const int heads = min(P.G - u.head0 - H * g, H);        // may be <= 0
-        const int64_t head_at = (int64_t)u.row * P.G + u.head0 + H * g;
-        const bool row_ok = idx_ok(u.row, P.rows, P.status);
         float l[H], mx[H];
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             l[i] = 0.0f;
             if (kStats) mx[i] = -kInf;
         }
-        bool give_up = false, fresh = true;             // fresh: a head has no reference yet
-        const float *ah = T->ah[nu & (kAhRing - 1)] + H * g;
+        bool fresh = true;                              // a head has no reference yet
+        const float *ah = T->ah[nu & (kAhRing - 1)] + col;
         const float *ref = T->ref[g];
-        for (int j = 0; j < tiles; ++j, ++kt, tr.next(kTileRing)) {
-            const uint32_t b = kt & 1u;
-            ok = ok && wait_lane(bars.scales_full(tr.idx), tr.phase, abort_flag);
+        for (int j = 0; j < tiles; ++j, ++kt) {
+            const uint32_t b = kt & 1u, tr = kt & (kTileRing - 1);
+            ok = ok && wait_lane(bars.scales_full(tr), (kt / kTileRing) & 1u, abort_flag);
             // an entry that selects nothing, or whose scale is out of range, has scale 0 and a weight
             // of 2^-inf
-            float d = ok ? T->descale[tr.idx][key] : 0.0f;
+            float d = ok ? T->descale[tr][key] : 0.0f;
             if (!(d >= kMinDescale && d <= kMaxDescale)) {
                 bad |= ok && __float_as_uint(d) != kNoKey;
                 d = 0.0f;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars.looked_up(tr.idx));
+            if (lane == 0) mbar_arrive(bars.looked_up(tr));
             const float log2d = log2f(d), inv_d = d > 0.0f ? __frcp_rn(d) : 0.0f;
             ok = ok && wait_lane(bars.s_full(b), (kt >> 1) & 1u, abort_flag);
             float t[H];                                 // y - ref, the weights' exponents
             __syncwarp();
             tc_fence_after();
-            {
-                uint32_t hi[H], lo[H], rp[H];
-                const uint32_t s = tmem + lanes + b * kSCols<N> + H * g;
+#pragma unroll
+            for (int h = 0; h < H; h += 8) {
+                uint32_t hi[8], lo[8], rp[8];
+                const uint32_t s = tmem + lanes + b * kSCols<N> + col + h;
                 tmem_ld_nowait(s, hi);
                 tmem_ld_nowait(s + N, lo);
                 if (P.has_rope) tmem_ld_nowait(s + 2 * N, rp);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < H; i += 4) {
+                for (int i = 0; i < 8; i += 4) {
                     float a4[4];
-                    lds4(ah + i, a4);
+                    lds4(ah + h + i, a4);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float sc = fmaf(__uint_as_float(lo[i + k]), 0.0625f, __uint_as_float(hi[i + k]));
-                        t[i + k] = fmaf(sc, d * a4[k], P.has_rope ? rs * __uint_as_float(rp[i + k]) : 0.0f);
+                        t[h + i + k] = fmaf(sc, d * a4[k], P.has_rope ? rs * __uint_as_float(rp[i + k]) : 0.0f);
                     }
                 }
             }
@@ -764,34 +756,35 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
             }
             const bool any = __any_sync(0xffffffffu, top > kTop || (fresh && d > 0.0f));
             const bool all = __all_sync(0xffffffffu, ok);
-            if (lane == 0) T->vote[g][b][q] = (any ? 1 : 0) | (all ? 0 : 2);
+            if (lane == 0) T->vote[g][turn & 1][q] = (any ? 1 : 0) | (all ? 0 : 2);
             named_bar(bar_id, 128);
-            const int4 v4 = *reinterpret_cast<const int4 *>(T->vote[g][b]);
+            const int4 v4 = *reinterpret_cast<const int4 *>(T->vote[g][turn++ & 1]);
             const int v = v4.x | v4.y | v4.z | v4.w;
-            if (v & 2) { give_up = true; break; }
+            if (v & 2) {
+                failed = true;
+                break;
+            }
             if (v & 1) {
-                // references with a larger weight than 2^kShift move to it, and a head's first one
-                // to its largest weight whatever it is; O and the sums follow
+                // references with a larger weight than 2^kTop move so that it is 2^kShift, and a head's
+                // first one so whatever its largest weight is; O and the sums follow
                 const float m = transpose_reduce<true>(t, lane);
-                if ((lane & (32 / H - 1)) == 0) T->red[g][lane / (32 / H)][q] = m;
+                if (holds) T->red[g][held][q] = m;
                 named_bar(bar_id, 128);
                 if (q == 0 && lane < H) {
                     float m4[4];
                     lds4(T->red[g][lane], m4);
                     const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     const bool seen = T->seen[g][lane] != 0;
-                    float up = seen ? fmaxf(most - kShift, 0.0f) : most > -kInf ? most - kShift : 0.0f;
+                    const float up = seen ? fmaxf(most - kShift, 0.0f) : most > -kInf ? most - kShift : 0.0f;
                     T->ref[g][lane] += up;
                     T->alpha[g][lane] = seen ? exp2_(-up) : 0.0f;   // nothing is summed before the first
                     T->moved[g][lane] = up;
                     T->seen[g][lane] = seen || most > -kInf;
-                    const uint32_t mask = (1u << H) - 1u;
-                    const bool all = __all_sync(mask, seen || most > -kInf);
-                    if (lane == 0) T->fresh[g] = !all;
+                    const bool all_seen = __all_sync((1u << H) - 1u, seen || most > -kInf);
+                    if (lane == 0) T->fresh[g] = !all_seen;
                 }
                 named_bar(bar_id, 128);
                 fresh = T->fresh[g] != 0;
-                uint32_t al[H];
 #pragma unroll
                 for (int i = 0; i < H; i += 4) {
                     float a4[4], u4[4];
@@ -799,29 +792,28 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                     lds4(T->moved[g] + i, u4);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        al[i + k] = __float_as_uint(a4[k]);
                         l[i + k] *= a4[k];
                         t[i + k] -= u4[k];
                     }
                 }
-                if (j > 0) {
+                if (j > 0) {                            // O holds the tiles before
                     ok = ok && wait_lane(bars.p_empty(b ^ 1u), ((kt - 1) >> 1) & 1u, abort_flag);
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < P.blocks; ++c) {
-                        const uint32_t o = tmem + lanes + 2 * kSCols<N> + c * 2 * N + H * g;
-                        uint32_t hi[H], lo[H];
-                        tmem_ld_nowait(o, hi);
-                        tmem_ld_nowait(o + N, lo);
+                    for (int c = 0; c < 2 * P.blocks; ++c) {        // hi and lo of each block
+                        const uint32_t o = tmem + lanes + 2 * kSCols<N> + c * N + col;
+                        uint32_t x[H];
+                        tmem_ld_nowait(o, x);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < H; ++i) {
-                            hi[i] = __float_as_uint(__uint_as_float(hi[i]) * __uint_as_float(al[i]));
-                            lo[i] = __float_as_uint(__uint_as_float(lo[i]) * __uint_as_float(al[i]));
+                        for (int i = 0; i < H; i += 4) {
+                            float a4[4];
+                            lds4(T->alpha[g] + i, a4);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) x[i + k] = __float_as_uint(__uint_as_float(x[i + k]) * a4[k]);
                         }
-                        tmem_st_nowait(o, hi);
-                        tmem_st_nowait(o + N, lo);
+                        tmem_st_nowait(o, x);
                     }
                     tmem_wait_st();
                     tc_fence_before();
@@ -848,10 +840,10 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                     lo[i / 4] = l8;
                 }
             }
-            uint8_t *pb = smem + P.p_off + b * (2 * N * 128);
+            uint8_t *pb = smem + P.p_off + b * (2 * N * kKeys);
             if constexpr (H == 8) {
-                *reinterpret_cast<uint2 *>(pb + weights_at<N>(key, 0) + 8 * g) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2 *>(pb + weights_at<N>(key, 1) + 8 * g) = make_uint2(lo[0], lo[1]);
+                *reinterpret_cast<uint2 *>(pb + weights_at<N>(key, 0) + col) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2 *>(pb + weights_at<N>(key, 1) + col) = make_uint2(lo[0], lo[1]);
             } else {
                 *reinterpret_cast<uint4 *>(pb + weights_at<N>(key, g)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4 *>(pb + weights_at<N>(key, 2 + g)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -859,53 +851,52 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
             fence_async_smem();
             mbar_arrive(bars.p_full(b));
         }
-        if (give_up) break;
-        // the unit's sums and maxima over the group's 128 keys
+        if (failed) break;
+        // the group's sums and maxima over its keys, and the unit's last value product
         if (tiles > 0) {
             const float ws = transpose_reduce<false>(l, lane);
             float wm = 0.0f;
             if constexpr (kStats) wm = transpose_reduce<true>(mx, lane);
-            if ((lane & (32 / H - 1)) == 0) {
-                T->lsum[g][lane / (32 / H)][q] = ws;
-                if (kStats) T->mx[g][lane / (32 / H)][q] = wm;
+            if (holds) {
+                T->lsum[g][held][q] = ws;
+                if (kStats) T->mx[g][held][q] = wm;
             }
             ok = ok && wait_lane(bars.p_empty((kt - 1) & 1u), ((kt - 1) >> 1) & 1u, abort_flag);
             __syncwarp();
-            tc_fence_after();
             named_bar(bar_id, 128);
-            ++nu;
         }
-#pragma unroll
-        for (int i = 0; i < H; ++i) {
-            float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (tiles > 0) lds4(T->lsum[g][i], s4);
-            const float s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-            l[i] = u.part >= 0 ? 1.0f : s == 0.0f ? 0.0f : 1.0f / s;
-        }
-        if (q == 0 && lane < heads && row_ok && (u.part >= 0 || kStats)) {
-            float s = 0.0f, m = -kInf, r = kNoRef;
+        const int heads = min(P.G - u.head0 - col, H);          // may be <= 0
+        const int64_t head_at = (int64_t)u.row * P.G + u.head0 + col;
+        const bool row_ok = idx_ok(u.row, P.rows, P.status);
+        if (q == 0 && lane < H) {
+            float r = kNoRef, s = 0.0f, m = -kInf;
             if (tiles > 0) {
-                float s4[4], m4[4];
+                float s4[4];
                 lds4(T->lsum[g][lane], s4);
                 s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-                if constexpr (kStats) {
-                    lds4(T->mx[g][lane], m4);
-                    m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                }
                 if (T->seen[g][lane]) r = ref[lane];
+                if constexpr (kStats) {
+                    lds4(T->mx[g][lane], s4);
+                    m = fmaxf(fmaxf(s4[0], s4[1]), fmaxf(s4[2], s4[3]));
+                }
             }
-            if (u.part >= 0) {
-                float *st = P.part_stat + ((int64_t)u.part * N + H * g + lane) * 3;
-                st[0] = r;
-                st[1] = s;
-                st[2] = m;
-            } else {
-                P.smax[head_at + lane] = m > -kInf ? m * kLn2 : m;
-                P.ssum[head_at + lane] = m > -kInf ? s * exp2_(r - m) : s;
+            T->coef[g][lane] = u.part >= 0 ? 1.0f : s == 0.0f ? 0.0f : 1.0f / s;
+            if (lane < heads && row_ok) {
+                if (u.part >= 0) {
+                    float *st = P.part_stat + ((int64_t)u.part * N + col + lane) * 3;
+                    st[0] = r;
+                    st[1] = s;
+                    st[2] = m;
+                } else if (kStats) {
+                    P.smax[head_at + lane] = m > -kInf ? m * kLn2 : m;
+                    P.ssum[head_at + lane] = m > -kInf ? s * exp2_(r - m) : s;
+                }
             }
         }
+        named_bar(bar_id, 128);
+        tc_fence_after();
         // O out of TMEM: pieces of a unit as they are in fp32, whole units normalised as bf16
-        float *po = P.part_o + ((int64_t)u.part * N + H * g) * P.Dm + key;
+        float *po = P.part_o + ((int64_t)u.part * N + col) * P.Dm + key;
         // neighbouring lanes exchange halves: an even lane stores two dims of the even heads, an odd
         // lane of the odd heads
         uint16_t *out = P.out + (head_at + (lane & 1)) * P.Dm + (key & ~1);
@@ -916,13 +907,18 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
             for (int i = 0; i < H; ++i) o[i] = 0.0f;
             if (tiles > 0) {
                 uint32_t hi[H], lo[H];
-                const uint32_t at = tmem + lanes + 2 * kSCols<N> + c * 2 * N + H * g;
+                const uint32_t at = tmem + lanes + 2 * kSCols<N> + c * 2 * N + col;
                 tmem_ld_nowait(at, hi);
                 tmem_ld_nowait(at + N, lo);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < H; ++i)
-                    o[i] = l[i] * fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(hi[i]));
+                for (int i = 0; i < H; i += 4) {
+                    float f4[4];
+                    lds4(T->coef[g] + i, f4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        o[i + k] = f4[k] * fmaf(__uint_as_float(lo[i + k]), 0.0625f, __uint_as_float(hi[i + k]));
+                }
                 if (c == P.blocks - 1) {                // the next unit's product may start
                     tc_fence_before();
                     __syncwarp();
@@ -945,6 +941,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 }
             }
         }
+        if (tiles > 0) ++nu;
         named_bar(bar_id, 128);         // sums, maxima and references are read before they are reset
     }
     T->abort_flag = 1;
@@ -965,13 +962,13 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars.u_full(i), 1);
             mbar_init(bars.u_empty(i), 2 + R::kSoft + R::kPrep + kGatherWarps);
-            mbar_init(bars.q_full(i), 32 * R::kPrep);
-            mbar_init(bars.q_empty(i), 1);
             mbar_init(bars.s_full(i), 1);
             mbar_init(bars.s_empty(i), R::kSoft);
             mbar_init(bars.p_full(i), 32 * R::kSoft);
             mbar_init(bars.p_empty(i), 1);
         }
+        mbar_init(bars.q_full(), 32 * R::kPrep);
+        mbar_init(bars.q_empty(), 1);
         mbar_init(bars.o_empty(), R::kSoft);
         for (int i = 0; i < kTileRing; ++i) {
             mbar_init(bars.rows_full(i), 32);
@@ -983,16 +980,10 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const
             mbar_init(bars.slot_empty(i), 1);
         }
         T->abort_flag = 0;
-        if (P.split) {
-            const uint32_t total = (uint32_t)P.units * P.tiles, t = share(total, gridDim.x, blockIdx.x);
-            T->first = t / P.tiles;
-            T->first_tile = t - T->first * P.tiles;
-            T->end = share(total, gridDim.x, blockIdx.x + 1);
-        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     // the join may be launched now; it waits for this grid's end
-    if (P.split) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (P.cuts > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == R::kQk) {
         tmem_alloc(smem_u32(&T->tmem), P.tmem_cols);
         tmem_relinquish();
@@ -1025,26 +1016,20 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const
     }
 }
 
-// Joins the partial outputs of units that were cut between CTAs: with references r_i, sums l_i and
-// outputs o_i of the pieces, o = sum o_i 2^(r_i - r) / sum l_i 2^(r_i - r), r = max r_i. A unit
-// that lies in one CTA's share was written by it.
+// Joins the partial outputs of a selection's pieces: with references r_i, sums l_i and outputs o_i,
+// o = sum o_i 2^(r_i - r) / sum l_i 2^(r_i - r), r = max r_i.
 // It is launched while the first kernel runs (programmatic dependent launch) and waits for its end.
 // A block joins one head: four dims a thread, every warp with the weights of its own, all pieces'
 // reads in flight.
 constexpr int kJoinThreads = 128;
 static_assert(kMaxTopk / kKeys <= 64, "two pieces a lane");
-__global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __grid_constant__ Params P, int N, int grid) {
-    // rows are cut only where units x tiles x grid is far inside 32 bits
-    const uint32_t unit = blockIdx.x, total = (uint32_t)(P.units * P.tiles);
-    auto cta_of = [&](uint32_t t) { return (int)(((t + 1) * grid + total - 1) / total - 1); };
-    const int c0 = cta_of(unit * P.tiles), pieces = cta_of((unit + 1) * P.tiles - 1) - c0 + 1;
-    const int32_t row = unit / P.head_blocks, head0 = (int)(unit - row * P.head_blocks) * 32;
-    const int h = blockIdx.y, t = threadIdx.x, lane = t & 31;
-    if (pieces == 1 || head0 + h >= P.G || !idx_ok(row, P.rows, P.status)) return;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+__global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __grid_constant__ Params P, int N) {
+    const int32_t whole = blockIdx.x, row = P.by_heads.div(whole), head0 = (whole - row * P.head_blocks) * 32;
+    const int h = blockIdx.y, t = threadIdx.x, lane = t & 31, pieces = P.cuts;
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // by every block: what follows this grid relies on it
+    if (head0 + h >= P.G || !idx_ok(row, P.rows, P.status)) return;
     const float kInf = __int_as_float(0x7f800000);
-    // the unit's pieces: the first starts it (slot 1 of its CTA), the others continue (slot 0)
-    const auto slot = [&](int i) { return (int64_t)(2 * (c0 + i) + (i == 0)) * N + h; };
+    const auto slot = [&](int i) { return ((int64_t)whole * pieces + i) * N + h; };
     float r[2], l[2], w[2], most = kNoRef, m = -kInf, sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -1122,35 +1107,40 @@ bool cache_attn_plan(const li_cache_attn_args &a, CacheAttnPlan *p) {
     p->head_blocks = (a.G + 31) / 32;
     p->tiles = (a.topk + kKeys - 1) / kKeys;
     p->blocks = a.Dm / 128;
-    p->units = (int64_t)a.batch * a.s1 * p->head_blocks;
-    const int per_tile = p->blocks + (a.Dr > 0 ? 1 : 0);
-    p->q_bytes = (uint32_t)(p->blocks * 2 * p->N * 128 + (a.Dr > 0 ? p->N * 128 : 0));
-    const uint32_t p_bytes = 2u * 2u * p->N * 128u;
-    p->slots = 0;
-    const int64_t total = p->units * p->tiles;
-    p->split = p->units < 4 * (int64_t)sms && p->tiles > 1;
-    // whole units: two q buffers where two tiles still fit, so that a unit's q is ready when it starts;
-    // a CTA with a share has two or three units, and its keys want the room
-    for (int bufs = p->split ? 1 : 2; bufs >= 1; --bufs) {
-        const uint32_t off = bufs * p->q_bytes;
-        const uint32_t slot_off = (off + p_bytes + 1023u) / 1024u * 1024u;
-        if (slot_off >= kTailOff) continue;
-        int slots = (int)((kTailOff - slot_off) / kSlot);
-        slots = slots < kMaxSlots ? slots : kMaxSlots;
-        if (slots < 2 * per_tile) continue;
-        p->q_bufs = bufs;
-        p->p_off = off;
-        p->slot_off = slot_off;
-        p->slots = slots;
-        break;
+    const int64_t whole = (int64_t)a.batch * a.s1 * p->head_blocks;
+    // Pieces per selection: the least time for the busiest CTA, in tiles, where a unit costs two more
+    // (its start and output) and the join two.
+    // 16 heads, 2048 entries a row, cut against whole: 1 row 13.1 and 29.5 us, 16 rows 15.7 and 28.9,
+    // 74 rows 24.8 and 33.2, 200 rows 66.0 and 67.5; 512 entries: 1 row 10.1 and 11.5. Cuts that the
+    // rule leaves out: 148 rows 40.1 against 38.3 us, 74 rows of 512 entries 15.2 against 13.0. Pieces
+    // of equal shares across the rows' ends took 26 to 31 us where equal pieces of a row take 25
+    int64_t best = INT64_MAX;
+    p->cuts = 1;
+    p->chunk = p->tiles;
+    for (int k = 1; k <= p->tiles && (k == 1 || whole * k <= 4 * (int64_t)sms); ++k) {
+        const int chunk = (p->tiles + k - 1) / k;
+        if ((p->tiles + chunk - 1) / chunk != k) continue;
+        const int64_t time = (whole * k + sms - 1) / sms * (chunk + 2) + (k > 1 ? 2 : 0);
+        if (time < best) {
+            best = time;
+            p->cuts = k;
+            p->chunk = chunk;
+        }
     }
-    if (p->slots == 0) return false;
+    p->units = whole * p->cuts;
+    // q, the weights of two tiles, and as many slots for keys as there is room for. A second buffer for
+    // the next unit's q takes the room of two slots (2048 tokens 201 us against 186)
+    const int per_tile = p->blocks + (a.Dr > 0 ? 1 : 0);
+    p->p_off = (uint32_t)(p->blocks * 2 * p->N * 128 + (a.Dr > 0 ? p->N * 128 : 0));
+    p->slot_off = (p->p_off + 2u * 2u * p->N * 128u + 1023u) / 1024u * 1024u;
+    p->slots = p->slot_off < kTailOff ? (int)((kTailOff - p->slot_off) / kSlot) : 0;
+    if (p->slots > kMaxSlots) p->slots = kMaxSlots;
+    if (p->slots < 2 * per_tile) return false;
     uint32_t cols = 32;
     while (cols < (uint32_t)(8 * p->N + 2 * p->N * p->blocks)) cols <<= 1;
     p->tmem_cols = cols;
-    const int64_t most = p->split ? total : p->units;
-    p->grid = (int)(most < sms ? most : sms);
-    p->partial_floats = p->split ? (size_t)2 * p->grid * p->N * (a.Dm + 3) : 0;
+    p->grid = (int)(p->units < sms ? p->units : sms);
+    p->partial_floats = p->cuts > 1 ? (size_t)p->units * p->N * (a.Dm + 3) : 0;
     return true;
 }
 
@@ -1168,9 +1158,9 @@ cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnP
     P.out = static_cast<uint16_t *>(out);
     P.smax = smax;
     P.ssum = ssum;
-    if (p.split) {
+    if (p.cuts > 1) {
         P.part_o = partial;
-        P.part_stat = partial + (size_t)2 * p.grid * p.N * a.Dm;
+        P.part_stat = partial + (size_t)p.units * p.N * a.Dm;
     }
     if (a.layout_k == LI_LAYOUT_PA_BSND) {
         P.block_table = a.block_table;
@@ -1198,10 +1188,10 @@ cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnP
     P.head_blocks = p.head_blocks;
     P.by_heads = FixedDiv(p.head_blocks);
     P.tiles = p.tiles;
-    P.split = p.split;
-    P.q_bufs = p.q_bufs;
+    P.cuts = p.cuts;
+    P.chunk = p.chunk;
+    P.by_cuts = FixedDiv(p.cuts);
     P.slots = p.slots;
-    P.q_bytes = p.q_bytes;
     P.p_off = p.p_off;
     P.slot_off = p.slot_off;
     P.tmem_cols = p.tmem_cols;
@@ -1210,17 +1200,17 @@ cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnP
                                       : launch_main<16, false>(P, p.grid, st))
                               : (smax ? launch_main<32, true>(P, p.grid, st)
                                       : launch_main<32, false>(P, p.grid, st));
-    if (e != cudaSuccess || !p.split) return e;
+    if (e != cudaSuccess || p.cuts == 1) return e;
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)p.units, (unsigned)(a.G < 32 ? a.G : 32));
+    cfg.gridDim = dim3((unsigned)(p.units / p.cuts), (unsigned)(a.G < 32 ? a.G : 32));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel, P, p.N, p.grid);
+    return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel, P, p.N);
 }
 
 }  // namespace li

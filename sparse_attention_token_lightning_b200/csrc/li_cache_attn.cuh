@@ -10,14 +10,14 @@ struct CacheAttnPlan {
     int N;                      // heads per CTA, padded (16 or 32): MMA N is 2 N (hi and lo parts)
     int head_blocks;            // CTAs' head ranges per row
     int tiles;                  // 128-entry tiles of a row's selection
-    int64_t units;              // rows x head_blocks
+    int cuts, chunk;            // pieces of a selection, and tiles of each
+    int64_t units;              // rows x head_blocks x cuts
     int grid;
-    int split;                  // 1: each CTA takes an equal range of all units' tiles
     int blocks;                 // 128-dim blocks of a key (Dm / 128)
-    int q_bufs, slots;
-    uint32_t q_bytes, p_off, slot_off;
+    int slots;
+    uint32_t p_off, slot_off;
     uint32_t tmem_cols;
-    size_t partial_floats;      // split: partial outputs and statistics in the workspace
+    size_t partial_floats;      // pieces: their outputs and statistics, in the workspace
 };
 
 // False when the argument set does not fit the kernel.

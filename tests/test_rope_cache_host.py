@@ -201,9 +201,9 @@ def test_cache_attention_outputs_workspace_and_limits(L):
     size = L.li_cache_attention_workspace_size
     # one tile of selected keys a row is never cut: no workspace; two tiles may be
     assert size(ctypes.byref(_cattn(topk=128)), ctypes.byref(n)) == 0 and n.value == 0
-    assert size(ctypes.byref(_cattn(topk=129)), ctypes.byref(n)) == 0 and n.value % 256 == 0 and n.value > 0
+    assert size(ctypes.byref(_cattn(topk=513)), ctypes.byref(n)) == 0 and n.value % 256 == 0 and n.value > 0
     need = n.value
-    run = lambda ws, b, out, m=None, s=None: L.li_cache_attention(ctypes.byref(_cattn(topk=129)), ws, b, out, m, s, None)  # noqa: E731
+    run = lambda ws, b, out, m=None, s=None: L.li_cache_attention(ctypes.byref(_cattn(topk=513)), ws, b, out, m, s, None)  # noqa: E731
     assert run(None, need, 0x200000) == 3 and run(0x100010, need, 0x200000) == 3
     assert run(0x100000, need - 256, 0x200000) == 3
     assert run(0x100000, need, None) == 1 and run(0x100000, need, 0x200008) == 1
