@@ -28,10 +28,18 @@
 //   lookup    each selected key's cache row for the gather and its scale for the softmax warps, a few
 //             tiles ahead, and how many tiles a unit has
 //   gather    copies codes and rope part with cp.async into 16 KB slots (128 keys x 128 bytes,
-//             128-byte swizzle); rows that select nothing are zero-filled. TMA's gather of four rows
-//             takes as long (attention of 64 single tokens 30.2 us against 30.9, one token 13.2 against
-//             12.8, 2048 tokens 205 against 204) and wants tensor maps from the host
+//             128-byte swizzle); rows that select nothing are zero-filled
 //   qk, pv    one thread each issues the two products
+// Measured (576 values a key, 16 heads; graph replay on one B200): 64 sequences x 2048 keys 26.7 us (85 MB
+// of selected rows, 3.2 TB/s; what memory alone takes is 13.3), one sequence 13, causal 2048 tokens x 1024
+// keys 172 us (1.05 GB out of L2, 6.1 TB/s), 21 rows x 777 keys x 128 heads of 256 19.5 us.
+// A tile then costs a CTA some 3700 cycles, of which no unit is full: the gather alone takes 2140 (38
+// bytes a cycle and SM, for 16 SMs as for 148), the operands of the products 150 KB of shared memory
+// (1500 cycles), a softmax from scores to weights 2000. More overlap did not help: with tiles of 64 keys
+// the 2048 tokens took 247 us where these took 205, with twice the softmax warps on alternate tiles 209
+// against 184, with eight gather warps 183, with TMA's gather for two of five slots more than either.
+// Shorter code did: the roles' code shares the instruction caches, and its loops are kept (226 us at 110
+// KB of code, 205 at 87, 184 at 79, 172 at 74), as did room for more slots (201 against 186).
 // Every wait is bounded in time; on expiry the kernel records LI_DEVERR_TIMEOUT and returns. The
 // softmax warps of a group agree on giving up (the vote carries it), so none is left at a barrier.
 #include <atomic>
@@ -514,9 +522,8 @@ __device__ void gather_role(const Params &P, uint8_t *smem, Tail *T, const Bars 
                 }
                 sr.next(P.slots);
             }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (c >= P.blocks || !there) break;     // a slot that is not free is not written
+#pragma unroll 1
+            for (int c = 0; c < P.blocks && there; ++c) {       // a slot that is not free is not written
                 there = wait_lane(bars.slot_empty(sr.idx), sr.phase ^ 1u, &T->abort_flag);
                 if (!there) break;
                 const uint32_t to = dst + sr.idx * kSlot;
@@ -576,9 +583,9 @@ __device__ void qk_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
                     }
                     next();
                 }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c >= P.blocks || !ok) break;
+#pragma unroll 1
+                for (int c = 0; c < P.blocks; ++c) {
+                    if (!ok) break;
                     ok = wait_lane(bars.slot_full(slot), phase, &T->abort_flag);
                     if (!ok) break;
                     fence_async_smem();
@@ -625,7 +632,7 @@ __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
             if (elect_one()) {
                 int slot = sr.idx + P.has_rope;
                 if (slot == P.slots) slot = 0;
-#pragma unroll 4
+#pragma unroll 1
                 for (int c = 0; c < P.blocks; ++c) {
                     const uint64_t v = sw128_desc_mn(slots + slot * kSlot, kSlot);
                     const uint32_t d = tmem + 2 * kSCols<N> + c * 2 * N;
