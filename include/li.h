@@ -432,7 +432,7 @@ li_status li_sparse_attention(const li_attn_args *args, void *workspace, size_t 
  *              must be distinct and must not overlap those of x.
  *   positions  [rows] int32 or int64 (position_bits 32 or 64), any sign
  *   freq       radians per position of each pair, in double (li_rope_frequencies fills them);
- *              angles are reduced in double, so far positions keep their fp32 accuracy
+ *              angles are reduced in double, so positions up to 2^28 keep fp32 accuracy
  * Limits: rope_dim even in [2, 256], 0 <= rope_offset <= head_dim - rope_dim, head_dim <= 4096,
  * heads in [1, 1024], rows <= 2^31-1. Pointers are aligned to their element. 16-byte aligned data
  * (pointers, strides, rope_offset; in the half layout also rope_dim / 2) moves in 16-byte
@@ -565,13 +565,16 @@ li_status li_cache_read(const li_cache_args *args, void *stream);
  * Limits: G in [1, 128], Dm in {128, 256, 384, 512}, Dr in {0, 64}, topk in [1, 8192], S2 >= 1
  * when there are rows, scale positive and finite; q, q_rope, codes, k_rope 16-byte aligned, the
  * rest to their elements.
- * Numerics: q and the softmax weights enter the products as two E4M3 parts each (8 and 9
- * significant bits), the codes as they are, sums in fp32; the scores are exact to fp32 rounding,
- * the weights to 2^-9 relative, the normaliser sums the unrounded weights.
+ * Numerics: q and the softmax weights enter the products as two E4M3 parts each, the codes as they
+ * are, sums in fp32. q is exact down to 2^-13 of its head's largest element and off by at most 2^-21
+ * of that below, so the scores have fp32 accuracy; a weight exp(x - m) descale_s is off by at most
+ * 1.25 x 2^-9 of itself or 2^-18 of the row's largest, whichever is more; the normaliser sums the
+ * unrounded weights.
  * The workspace (li_cache_attention_workspace_size bytes, 256-byte aligned; it depends on the
- * current device's SM count, and may be NULL where that is 0) holds partial outputs when a few rows
- * are cut between SMs; contents on entry are ignored, and calls that may overlap need their own. Stream-ordered, no allocation,
- * graph-capturable, deterministic (bit-identical reruns on one device model).
+ * current device's SM count, and may be NULL where that is 0) holds partial outputs when few rows
+ * are cut between SMs; contents on entry are ignored, and calls that may overlap need their own.
+ * Stream-ordered, no allocation, graph-capturable, deterministic (bit-identical reruns on one
+ * device model).
  */
 typedef struct li_cache_attn_args {
     const void *q, *q_rope;                 /* bf16                                               */

@@ -8,11 +8,11 @@
 // to fp32 rounding:
 //   q       times a power of two per head (largest element in [128, 256)) = hi + lo / 16, hi and
 //           lo in E4M3: 8 bits in 4 + 4, so every bf16 element down to 2^-13 of the row's largest
-//           is held exactly (and none is off by more than 2^-22 of it)
-//   weights with y = x log2(e) + log2(d_s), 2^(y - ref) = hi + lo / 16 likewise (9 bits, half the
-//           error of a bf16 weight). The reference follows the largest y, not the largest x, so the
-//           scale is inside the exponent and the parts are full where the products are large; the
-//           normaliser sums 2^(y - ref) / d_s in fp32.
+//           is held exactly (and none is off by more than 2^-21 of it)
+//   weights with y = x log2(e) + log2(d_s), 2^(y - ref) = hi + lo / 16 likewise (9 bits by way of
+//           fp16's 11: 1.25 x 2^-9, less than a bf16 weight's 2^-8). The reference follows the
+//           largest y, not the largest x, so the scale is inside the exponent and the parts are
+//           full where the products are large; the normaliser sums 2^(y - ref) / d_s in fp32.
 // The products S = K Q^T (keys on M = 128, hi and lo heads on N) and O^T += V^T P^T (dims on M = 128,
 // the key tile read MN-major, keys on K) both read the same gathered tile; the rope part is a bf16
 // product of its own into other TMEM columns, since its codes have no scale.

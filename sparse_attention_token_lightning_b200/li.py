@@ -547,11 +547,6 @@ def _empty_like(t, stream):
         return torch.empty_like(t)
 
 
-def _on(t, dev, name):
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got a tensor on {t.device}")
-
-
 def _ptr_of(t, dev, name, dtype, shape):
     """Address of a contiguous tensor on `dev` of the given type and shape."""
     if t.device != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
