@@ -164,6 +164,47 @@ def test_the_bounds_checked_build_agrees(monkeypatch):
         assert torch.equal(u, v)
 
 
+def test_offsets_past_32_bits():
+    """Rows whose codes, rope parts and strided source lie beyond 2^32 bytes of their buffers."""
+    nb, block, dim = 140_000, 64, 512                       # 4.6 GB of codes
+    if torch.cuda.mem_get_info()[0] < 20e9:
+        pytest.skip("needs 20 GB")
+    codes = torch.empty(nb, block, 1, dim, dtype=torch.float8_e4m3fn, device="cuda")
+    scales = torch.empty(nb, block, device="cuda")
+    kr = torch.empty(nb, block, 1, 64, dtype=torch.bfloat16, device="cuda")
+    n, g = 200, torch.Generator().manual_seed(7)
+    assert (nb - 5) * block * dim > 2 ** 32
+    table = torch.tensor([[nb - 1, 0, nb - 3, nb - 2]], dtype=torch.int32, device="cuda")
+    src = torch.empty(n, 12_000_000, dtype=torch.bfloat16, device="cuda")       # rows 24 MB apart: 4.8 GB
+    x, r = src[:, -576:-64], src[:, -64:]
+    x.copy_(torch.randn(n, dim, generator=g))
+    r.copy_(torch.randn(n, 64, generator=g))
+    lens, cu = torch.tensor([n], dtype=torch.int32).cuda(), torch.tensor([0, n], dtype=torch.int32).cuda()
+    li.cache_write(x, codes, scales, rope=r, rope_cache=kr, seqused_k=lens, block_table=table, cu_seqlens=cu)
+    want, s = ref.quantise(x.cpu())
+    at = torch.tensor([slot for _, slot in ref.places([n], table.tolist(), block, cu=[0, n])]).cuda()
+    got = codes.view(torch.uint8).view(-1, dim)[at]
+    assert torch.equal(got.cpu(), want) and torch.equal(scales.view(-1)[at].cpu(), s)
+    assert torch.equal(kr.view(-1, 64)[at], r)
+    back, rope = torch.zeros_like(src[:, :512]), torch.zeros_like(src[:, :64])
+    li.cache_read(codes, scales, back, rope_cache=kr, rope_out=rope, seqused_k=lens, block_table=table, cu_seqlens=cu)
+    assert torch.equal(back.cpu(), (got.view(torch.float8_e4m3fn).cpu().float() * s[:, None]).to(torch.bfloat16))
+    assert torch.equal(rope, r)
+    q, qr = (torch.randn(1, 2, 16, d, generator=g).to(torch.bfloat16) for d in (512, 64))
+    idx = torch.stack([torch.randperm(n, generator=g)[:150] for _ in range(2)]).view(1, 2, 1, 150).int()
+    out = li.cache_attention(q.cuda(), codes, scales, idx.cuda(), 0.05, q_rope=qr.cuda(), rope_cache=kr,
+                             block_table=table, s2=n)
+    small = torch.tensor([[0, 1, 2, 3]], dtype=torch.int32)         # the same keys in a small cache
+    pick = lambda t: t[table[0].long()].cpu()  # noqa: E731
+    p = cache_attn_ref.CacheAttn(q, pick(codes.view(torch.uint8)).view(torch.float8_e4m3fn), pick(scales), idx, 0.05,
+                                 qr, pick(kr), small, n)
+    cache_attn_ref.check(p, out, label="far rows")
+    freqs = li.rope_frequencies(64)
+    pos = torch.arange(n, device="cuda")
+    y = li.rope(r.unsqueeze(1), pos, freqs, out=torch.empty_like(src)[:, :64].unsqueeze(1))
+    _rotated(y, r.unsqueeze(1), pos, freqs, 0, False)
+
+
 FIRST_CAPTURE = """
 import sys
 sys.path[:0] = [{root!r}, {tests!r}]
