@@ -570,11 +570,8 @@ li_status li_cache_read(const li_cache_args *args, void *stream);
  * of that below, so the scores have fp32 accuracy; a weight exp(x - m) descale_s is off by at most
  * 1.25 x 2^-9 of itself or 2^-18 of the row's largest, whichever is more; the normaliser sums the
  * unrounded weights.
- * The workspace (li_cache_attention_workspace_size bytes, 256-byte aligned; it depends on the
- * current device's SM count, and may be NULL where that is 0) holds partial outputs when few rows
- * are cut between SMs; contents on entry are ignored, and calls that may overlap need their own.
- * Stream-ordered, no allocation, graph-capturable, deterministic (bit-identical reruns on one
- * device model).
+ * No workspace. Stream-ordered, no allocation, graph-capturable, deterministic (bit-identical reruns
+ * on one device model).
  */
 typedef struct li_cache_attn_args {
     const void *q, *q_rope;                 /* bf16                                               */
@@ -591,9 +588,8 @@ typedef struct li_cache_attn_args {
     int32_t num_blocks, block_size;         /* PA_BSND: >= 1 and 1..1024; else 0                  */
     int32_t reserved;                       /* must be 0                                          */
 } li_cache_attn_args;
-li_status li_cache_attention_workspace_size(const li_cache_attn_args *args, size_t *bytes);
-li_status li_cache_attention(const li_cache_attn_args *args, void *workspace, size_t workspace_bytes,
-                             void *out, float *softmax_max, float *softmax_sum, void *stream);
+li_status li_cache_attention(const li_cache_attn_args *args, void *out, float *softmax_max,
+                             float *softmax_sum, void *stream);
 
 /* Message of the last failing call on this host thread ("" if none). */
 const char *li_last_error_string(void);

@@ -197,10 +197,6 @@ li_status validate_cache_attn(const li_cache_attn_args *a, li::CacheAttnPlan *p)
     return LI_OK;
 }
 
-size_t cache_attn_bytes(const li::CacheAttnPlan &p) {
-    return li::align_up(p.partial_floats * sizeof(float), 256);
-}
-
 }  // namespace
 
 extern "C" {
@@ -280,30 +276,17 @@ li_status li_cache_read(const li_cache_args *args, void *stream) {
     return ok();
 }
 
-li_status li_cache_attention_workspace_size(const li_cache_attn_args *args, size_t *bytes) {
-    li::CacheAttnPlan p;
-    li_status st = validate_cache_attn(args, &p);
-    if (st != LI_OK) return st;
-    if (!bytes) return fail(LI_ERR_INVALID_ARG, "bytes is NULL");
-    *bytes = cache_attn_bytes(p);
-    return ok();
-}
-
-li_status li_cache_attention(const li_cache_attn_args *args, void *workspace, size_t workspace_bytes,
-                             void *out, float *softmax_max, float *softmax_sum, void *stream) {
+li_status li_cache_attention(const li_cache_attn_args *args, void *out, float *softmax_max, float *softmax_sum,
+                             void *stream) {
     NvtxRange range("li_cache_attention");
     li::CacheAttnPlan p;
     li_status st = validate_cache_attn(args, &p);
     if (st != LI_OK) return st;
-    const size_t need = cache_attn_bytes(p);
-    if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
-        return fail(LI_ERR_WORKSPACE, "workspace must be a 256-byte aligned device buffer of >= %zu bytes", need);
     if (p.units == 0) return ok();
     if (!out || !aligned(out, 16)) return fail(LI_ERR_INVALID_ARG, "out must be a 16-byte aligned device buffer");
     if ((softmax_max == nullptr) != (softmax_sum == nullptr) || !aligned(softmax_max, 4) || !aligned(softmax_sum, 4))
         return fail(LI_ERR_INVALID_ARG, "softmax_max and softmax_sum go together, 4-byte aligned");
-    cudaError_t e = li::launch_cache_attention(*args, p, static_cast<float *>(workspace), out, softmax_max,
-                                               softmax_sum, static_cast<cudaStream_t>(stream));
+    cudaError_t e = li::launch_cache_attention(*args, p, out, softmax_max, softmax_sum, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(LI_ERR_CUDA, "cache attention launch: %s", cudaGetErrorString(e));
     return ok();
 }

@@ -17,9 +17,9 @@
 // the key tile read MN-major, keys on K) both read the same gathered tile; the rope part is a bf16
 // product of its own into other TMEM columns, since its codes have no scale.
 //
-// One CTA per SM works in turn on units: a row, a block of up to 32 heads, and all tiles of 128 selected
-// keys or, when there are few rows (decode), one of several equal pieces of them; pieces leave partial
-// outputs, which a second kernel joins (cache_attn_plan says when). Warps:
+// One CTA per SM works in turn on units: a row, a block of up to 32 heads, and its tiles of 128 selected
+// keys. When there are few rows (decode) a cluster of two, four or eight CTAs shares each unit's tiles,
+// and joins its partial outputs through distributed shared memory (cache_attn_plan says when). Warps:
 //   softmax   two groups of 4 warps, each with half the heads: a thread owns one key of the tile and
 //             8 or 16 heads. The largest weight is set to 2^4 and may grow to 2^8 (E4M3 holds 448)
 //             before the reference moves; a vote per tile finds that out, and only then are the
@@ -30,16 +30,16 @@
 //   gather    copies codes and rope part with cp.async into 16 KB slots (128 keys x 128 bytes,
 //             128-byte swizzle); rows that select nothing are zero-filled
 //   qk, pv    one thread each issues the two products
-// Measured (576 values a key, 16 heads; graph replay on one B200): 64 sequences x 2048 keys 26.7 us (85 MB
-// of selected rows, 3.2 TB/s; what memory alone takes is 13.3), one sequence 13, causal 2048 tokens x 1024
-// keys 172 us (1.05 GB out of L2, 6.1 TB/s), 21 rows x 777 keys x 128 heads of 256 19.5 us.
+// Measured (576 values a key, 16 heads; graph replay on one B200): 64 sequences x 2048 keys 26.4 us (85 MB
+// of selected rows, 3.2 TB/s; what memory alone takes is 13.3), one sequence 12.5, causal 2048 tokens x 1024
+// keys 171 us (1.05 GB out of L2, 6.1 TB/s), 21 rows x 777 keys x 128 heads of 256 19.5 us.
 // A tile then costs a CTA some 3700 cycles, of which no unit is full: the gather alone takes 2140 (38
 // bytes a cycle and SM, for 16 SMs as for 148), the operands of the products 150 KB of shared memory
 // (1500 cycles), a softmax from scores to weights 2000. More overlap did not help: with tiles of 64 keys
 // the 2048 tokens took 247 us where these took 205, with twice the softmax warps on alternate tiles 209
 // against 184, with eight gather warps 183, with TMA's gather for two of five slots more than either.
 // Shorter code did: the roles' code shares the instruction caches, and its loops are kept (226 us at 110
-// KB of code, 205 at 87, 184 at 79, 172 at 74), as did room for more slots (201 against 186).
+// KB of code, 205 at 87, 184 at 79, 172 at 71), as did room for more slots (201 against 186).
 // Every wait is bounded in time; on expiry the kernel records LI_DEVERR_TIMEOUT and returns. The
 // softmax warps of a group agree on giving up (the vote carries it), so none is left at a barrier.
 #include <atomic>
@@ -60,6 +60,7 @@ using namespace sm100;
 
 constexpr int kKeys = 128;                          // selected keys per tile (MMA M)
 constexpr uint32_t kSlot = kKeys * 128;             // 128 bytes of 128 keys
+constexpr int kMaxCutLog2 = 3, kMaxCuts = 1 << kMaxCutLog2;     // CTAs that share a unit (portable clusters)
 constexpr int kMaxSlots = 16, kTileRing = 4, kAhRing = 4;
 constexpr int kGatherWarps = 4;
 constexpr uint32_t kSmemBytes = 232448;
@@ -89,7 +90,6 @@ struct Unit {
     int32_t row;            // -1: no more units
     int32_t head0;          // first head
     int32_t tile0, tiles;   // tiles of the row's selection
-    int32_t part;           // partial slot, or -1: the unit has the whole selection
 };
 
 // Barriers and small arrays in the shared-memory tail.
@@ -139,15 +139,14 @@ struct Params {
     uint32_t *status;
     uint16_t *out;
     float *smax, *ssum;
-    float *part_o, *part_stat;          // [units][N][Dm], [units][N][3]
     int64_t bt_stride, key_rows;
     int64_t units;
     float scale;
     int32_t rows, s1, s2, G, Dm, topk, block_size, num_blocks;
-    int32_t has_rope, blocks, head_blocks, tiles, cuts, chunk;     // cuts: pieces per selection, of chunk tiles
+    int32_t has_rope, blocks, head_blocks, tiles, cut_log2;    // CTAs per unit
     int32_t slots;
     uint32_t p_off, slot_off, tmem_cols;
-    FixedDiv by_block, by_s1, by_heads, by_cuts;
+    FixedDiv by_block, by_s1, by_heads;
 };
 
 struct Ring {
@@ -276,21 +275,35 @@ __device__ __forceinline__ float transpose_reduce(const float (&v)[H], int lane)
     return a[0];
 }
 
-// The it-th unit of this CTA.
+// The it-th unit of this CTA, or its share of one.
 __device__ __forceinline__ Unit unit_at(const Params &P, int it) {
-    Unit u{-1, 0, 0, P.tiles, -1};
-    const int64_t i = blockIdx.x + (int64_t)it * gridDim.x;
+    Unit u{-1, 0, 0, P.tiles};
+    const int64_t i = (blockIdx.x >> P.cut_log2) + (int64_t)it * (gridDim.x >> P.cut_log2);
     if (i >= P.units) return u;                         // below 2^26
-    int32_t whole = (int32_t)i;
-    if (P.cuts > 1) {
-        whole = P.by_cuts.div(whole);
-        u.tile0 = ((int32_t)i - whole * P.cuts) * P.chunk;
-        u.tiles = min(P.chunk, P.tiles - u.tile0);
-        u.part = (int32_t)i;
+    if (P.cut_log2) {
+        const int c = (int)blockIdx.x & ((1 << P.cut_log2) - 1);
+        u.tile0 = c * P.tiles >> P.cut_log2;
+        u.tiles = ((c + 1) * P.tiles >> P.cut_log2) - u.tile0;
     }
-    u.row = P.by_heads.div(whole);
-    u.head0 = (whole - u.row * P.head_blocks) * 32;
+    u.row = P.by_heads.div((int32_t)i);
+    u.head0 = ((int32_t)i - u.row * P.head_blocks) * 32;
     return u;
+}
+
+// ---- clusters ----------------------------------------------------------------------------------------
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Four floats at the same place as `addr` in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
 }
 
 // ---- lookups -----------------------------------------------------------------------------------------
@@ -653,6 +666,10 @@ __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
     T->abort_flag = 1;
 }
 
+// A share's partial outputs in shared memory, from slot_off on: O [N][Dm] in fp32, then per head its
+// reference, sum and maximum (16 bytes).
+template <int N> __device__ __forceinline__ uint32_t part_stat(int32_t Dm, int h) { return (uint32_t)(N * Dm + 4 * h) * 4u; }
+
 // ---- softmax and output ------------------------------------------------------------------------------
 // Four consecutive floats of shared memory.
 __device__ __forceinline__ void lds4(const float *p, float (&v)[4]) {
@@ -887,23 +904,19 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                     m = fmaxf(fmaxf(s4[0], s4[1]), fmaxf(s4[2], s4[3]));
                 }
             }
-            T->coef[g][lane] = u.part >= 0 ? 1.0f : s == 0.0f ? 0.0f : 1.0f / s;
-            if (lane < heads && row_ok) {
-                if (u.part >= 0) {
-                    float *st = P.part_stat + ((int64_t)u.part * N + col + lane) * 3;
-                    st[0] = r;
-                    st[1] = s;
-                    st[2] = m;
-                } else if (kStats) {
-                    P.smax[head_at + lane] = m > -kInf ? m * kLn2 : m;
-                    P.ssum[head_at + lane] = m > -kInf ? s * exp2_(r - m) : s;
-                }
+            T->coef[g][lane] = P.cut_log2 ? 1.0f : s == 0.0f ? 0.0f : 1.0f / s;
+            if (P.cut_log2) {
+                *reinterpret_cast<float4 *>(smem + P.slot_off + part_stat<N>(P.Dm, col + lane)) = make_float4(r, s, m, 0.0f);
+            } else if (kStats && lane < heads && row_ok) {
+                P.smax[head_at + lane] = m > -kInf ? m * kLn2 : m;
+                P.ssum[head_at + lane] = m > -kInf ? s * exp2_(r - m) : s;
             }
         }
         named_bar(bar_id, 128);
         tc_fence_after();
-        // O out of TMEM: pieces of a unit as they are in fp32, whole units normalised as bf16
-        float *po = P.part_o + ((int64_t)u.part * N + col) * P.Dm + key;
+        // O out of TMEM: a share of a unit as it is in fp32 to where its keys were (the CTA has no other
+        // unit, and the last product has read them), whole units normalised as bf16
+        float *po = reinterpret_cast<float *>(smem + P.slot_off) + col * P.Dm + key;
         // neighbouring lanes exchange halves: an even lane stores two dims of the even heads, an odd
         // lane of the odd heads
         uint16_t *out = P.out + (head_at + (lane & 1)) * P.Dm + (key & ~1);
@@ -932,11 +945,11 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                     if (lane == 0) mbar_arrive(bars.o_empty());
                 }
             }
-            if (u.part >= 0) {
-                // a piece without keys is told by its sum of 0; nothing else of it is read
+            if (P.cut_log2) {
+                // a share without keys is told by its sum of 0; nothing else of it is read
 #pragma unroll
                 for (int i = 0; i < H; ++i)
-                    if (i < heads && tiles > 0 && row_ok) po[(int64_t)i * P.Dm] = o[i];
+                    if (tiles > 0) po[i * P.Dm] = o[i];
             } else {
 #pragma unroll
                 for (int i = 0; i < H; i += 2) {
@@ -952,6 +965,55 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
         named_bar(bar_id, 128);         // sums, maxima and references are read before they are reset
     }
     T->abort_flag = 1;
+}
+
+// Joins the cluster's partial outputs of its unit: with references r_i, sums l_i and outputs o_i,
+// o = sum o_i 2^(r_i - r) / sum l_i 2^(r_i - r), r = max r_i. The CTAs share the outputs, four dims a
+// thread and turn; all shares' reads are in flight.
+template <int N, bool kStats>
+__device__ void join(const Params &P, uint8_t *smem) {
+    const int cuts = 1 << P.cut_log2, rank = (int)blockIdx.x & (cuts - 1);
+    const Unit u = unit_at(P, 0);
+    const uint32_t base = smem_u32(smem) + P.slot_off;
+    const float kInf = __int_as_float(0x7f800000);
+    if (!idx_ok(u.row, P.rows, P.status)) return;
+    const int items = min(P.G - u.head0, N) * (P.Dm / 4);
+    for (int t = rank * Roles<N>::kThreads + threadIdx.x; t < items; t += cuts * Roles<N>::kThreads) {
+        const int h = t / (P.Dm / 4), d = 4 * t - h * P.Dm;
+        float w[kMaxCuts], l[kMaxCuts], most = kNoRef, m = -kInf, sum = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v[kMaxCuts];
+#pragma unroll
+        for (int i = 0; i < kMaxCuts; ++i) {
+            if (i >= cuts) break;
+            const float4 st = ld_peer(base + part_stat<N>(P.Dm, h), i);
+            v[i] = ld_peer(base + (uint32_t)(h * P.Dm + d) * 4u, i);
+            w[i] = st.x;
+            l[i] = st.y;
+            m = fmaxf(m, st.z);
+            most = fmaxf(most, st.x);
+        }
+#pragma unroll
+        for (int i = 0; i < kMaxCuts; ++i) {
+            // a share without keys left no outputs: not even a NaN of what lies there may count
+            if (i >= cuts) break;
+            if (l[i] == 0.0f) continue;
+            w[i] = exp2_(w[i] - most);
+            sum = fmaf(l[i], w[i], sum);
+            o.x = fmaf(v[i].x, w[i], o.x);
+            o.y = fmaf(v[i].y, w[i], o.y);
+            o.z = fmaf(v[i].z, w[i], o.z);
+            o.w = fmaf(v[i].w, w[i], o.w);
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+        const int64_t at = (int64_t)u.row * P.G + u.head0 + h;
+        *reinterpret_cast<uint2 *>(P.out + at * P.Dm + d) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+        if (kStats && d == 0) {
+            P.smax[at] = m > -kInf ? m * kLn2 : m;
+            P.ssum[at] = m > -kInf ? sum * exp2_(most - m) : sum;
+        }
+    }
 }
 
 template <int N, bool kStats>
@@ -989,8 +1051,6 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const
         T->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    // the join may be launched now; it waits for this grid's end
-    if (P.cuts > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == R::kQk) {
         tmem_alloc(smem_u32(&T->tmem), P.tmem_cols);
         tmem_relinquish();
@@ -1021,68 +1081,12 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const
         tc_fence_after();
         tmem_dealloc(tmem, P.tmem_cols);
     }
-}
-
-// Joins the partial outputs of a selection's pieces: with references r_i, sums l_i and outputs o_i,
-// o = sum o_i 2^(r_i - r) / sum l_i 2^(r_i - r), r = max r_i.
-// It is launched while the first kernel runs (programmatic dependent launch) and waits for its end.
-// A block joins one head: four dims a thread, every warp with the weights of its own, all pieces'
-// reads in flight.
-constexpr int kJoinThreads = 128;
-static_assert(kMaxTopk / kKeys <= 64, "two pieces a lane");
-__global__ void __launch_bounds__(kJoinThreads) cache_attn_join_kernel(const __grid_constant__ Params P, int N) {
-    const int32_t whole = blockIdx.x, row = P.by_heads.div(whole), head0 = (whole - row * P.head_blocks) * 32;
-    const int h = blockIdx.y, t = threadIdx.x, lane = t & 31, pieces = P.cuts;
-    asm volatile("griddepcontrol.wait;" ::: "memory");      // by every block: what follows this grid relies on it
-    if (head0 + h >= P.G || !idx_ok(row, P.rows, P.status)) return;
-    const float kInf = __int_as_float(0x7f800000);
-    const auto slot = [&](int i) { return ((int64_t)whole * pieces + i) * N + h; };
-    float r[2], l[2], w[2], most = kNoRef, m = -kInf, sum = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        r[k] = kNoRef;
-        l[k] = 0.0f;
-        if (lane + 32 * k < pieces) {
-            const float *st = P.part_stat + slot(lane + 32 * k) * 3;
-            r[k] = st[0];
-            l[k] = st[1];
-            m = fmaxf(m, st[2]);
-        }
-        most = fmaxf(most, r[k]);
-    }
-    most = warp_max(most);
-    m = warp_max(m);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        w[k] = l[k] == 0.0f ? 0.0f : exp2_(r[k] - most);    // 0: a piece without keys
-        sum = fmaf(l[k], w[k], sum);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t at = (int64_t)row * P.G + head0 + h;
-    const bool mine = 4 * t < P.Dm;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = 0; i < pieces; ++i) {
-        const float f = __shfl_sync(0xffffffffu, i < 32 ? w[0] : w[1], i & 31);
-        // a piece without keys left nothing here: not even a NaN of what lies there may count
-        if (mine && f != 0.0f) {
-            const float4 v = *reinterpret_cast<const float4 *>(P.part_o + slot(i) * P.Dm + 4 * t);
-            o.x = fmaf(v.x, f, o.x);
-            o.y = fmaf(v.y, f, o.y);
-            o.z = fmaf(v.z, f, o.z);
-            o.w = fmaf(v.w, f, o.w);
-        }
-    }
-    if (mine) {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2 *>(P.out + at * P.Dm + 4 * t) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-    }
-    if (t == 0 && P.smax) {
-        P.smax[at] = m > -kInf ? m * kLn2 : m;
-        P.ssum[at] = m > -kInf ? sum * exp2_(most - m) : sum;
+    if (P.cut_log2) {               // every CTA of the cluster comes here, whatever became of its unit
+        __syncwarp();
+        cluster_sync();
+        join<N, kStats>(P, smem);
+        __syncwarp();
+        cluster_sync();             // its shared memory has been read
     }
 }
 
@@ -1102,8 +1106,18 @@ template <int N, bool kStats>
 cudaError_t launch_main(const Params &P, int grid, cudaStream_t st) {
     cudaError_t e = allow_smem<cache_attn_kernel<N, kStats>>();
     if (e != cudaSuccess) return e;
-    cache_attn_kernel<N, kStats><<<grid, Roles<N>::kThreads, kSmemBytes, st>>>(P);
-    return cudaGetLastError();
+    cudaLaunchAttribute cluster{};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = 1u << P.cut_log2;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(Roles<N>::kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = st;
+    cfg.attrs = &cluster;
+    cfg.numAttrs = P.cut_log2 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, cache_attn_kernel<N, kStats>, P);
 }
 
 }  // namespace
@@ -1114,27 +1128,19 @@ bool cache_attn_plan(const li_cache_attn_args &a, CacheAttnPlan *p) {
     p->head_blocks = (a.G + 31) / 32;
     p->tiles = (a.topk + kKeys - 1) / kKeys;
     p->blocks = a.Dm / 128;
-    const int64_t whole = (int64_t)a.batch * a.s1 * p->head_blocks;
-    // Pieces per selection: the least time for the busiest CTA, in tiles, where a unit costs two more
-    // (its start and output) and the join two.
-    // 16 heads, 2048 entries a row, cut against whole: 1 row 13.1 and 29.5 us, 16 rows 15.7 and 28.9,
-    // 74 rows 24.8 and 33.2, 200 rows 66.0 and 67.5; 512 entries: 1 row 10.1 and 11.5. Cuts that the
-    // rule leaves out: 148 rows 40.1 against 38.3 us, 74 rows of 512 entries 15.2 against 13.0. Pieces
-    // of equal shares across the rows' ends took 26 to 31 us where equal pieces of a row take 25
-    int64_t best = INT64_MAX;
-    p->cuts = 1;
-    p->chunk = p->tiles;
-    for (int k = 1; k <= p->tiles && (k == 1 || whole * k <= 4 * (int64_t)sms); ++k) {
-        const int chunk = (p->tiles + k - 1) / k;
-        if ((p->tiles + chunk - 1) / chunk != k) continue;
-        const int64_t time = (whole * k + sms - 1) / sms * (chunk + 2) + (k > 1 ? 2 : 0);
-        if (time < best) {
-            best = time;
-            p->cuts = k;
-            p->chunk = chunk;
-        }
-    }
-    p->units = whole * p->cuts;
+    p->units = (int64_t)a.batch * a.s1 * p->head_blocks;
+    // CTAs per unit: as many as leave every unit its SMs at once and every CTA a tile, if that spares
+    // a CTA two tiles or more. A cluster lies in one GPC, whose SMs do not divide by it: 74 clusters of
+    // two find room on 148 SMs, 33 of four and 15 of eight.
+    // Shared against whole, 16 heads: 1 row of 2048 entries 12.9 us and 29.2, 14 rows 13.7 and 29.2, 32
+    // rows (four CTAs each) 16.8 and 29.6, 74 rows (two) 23.9 and 32.2; 512 entries, 1 row 10.3 and
+    // 11.6, 74 rows 13.1 and 13.3. Where only one tile is spared sharing loses: 192 entries, 74 rows
+    // 11.4 and 9.8. Partial outputs through memory and a second kernel took 13.1, 15.7 (16 rows) and
+    // 24.8 us (74), with 5 us more on the host.
+    constexpr int kHalfSms[kMaxCutLog2 + 1] = {2, 4, 9, 20};    // half SMs that a cluster takes
+    p->cut_log2 = kMaxCutLog2;
+    while (p->cut_log2 > 0 && (p->units * kHalfSms[p->cut_log2] > 2 * (int64_t)sms || p->tiles >> p->cut_log2 == 0)) --p->cut_log2;
+    if (p->tiles - ((p->tiles + (1 << p->cut_log2) - 1) >> p->cut_log2) < 2) p->cut_log2 = 0;
     // q, the weights of two tiles, and as many slots for keys as there is room for. A second buffer for
     // the next unit's q takes the room of two slots (2048 tokens 201 us against 186)
     const int per_tile = p->blocks + (a.Dr > 0 ? 1 : 0);
@@ -1146,13 +1152,11 @@ bool cache_attn_plan(const li_cache_attn_args &a, CacheAttnPlan *p) {
     uint32_t cols = 32;
     while (cols < (uint32_t)(8 * p->N + 2 * p->N * p->blocks)) cols <<= 1;
     p->tmem_cols = cols;
-    p->grid = (int)(p->units < sms ? p->units : sms);
-    p->partial_floats = p->cuts > 1 ? (size_t)p->units * p->N * (a.Dm + 3) : 0;
+    p->grid = (int)(p->units < sms ? p->units << p->cut_log2 : sms);
     return true;
 }
 
-cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnPlan &p, float *partial,
-                                   void *out, float *smax, float *ssum, cudaStream_t st) {
+cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnPlan &p, void *out, float *smax, float *ssum, cudaStream_t st) {
     if (p.units == 0) return cudaSuccess;
     Params P{};
     P.q = static_cast<const uint16_t *>(a.q);
@@ -1165,10 +1169,6 @@ cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnP
     P.out = static_cast<uint16_t *>(out);
     P.smax = smax;
     P.ssum = ssum;
-    if (p.cuts > 1) {
-        P.part_o = partial;
-        P.part_stat = partial + (size_t)p.units * p.N * a.Dm;
-    }
     if (a.layout_k == LI_LAYOUT_PA_BSND) {
         P.block_table = a.block_table;
         P.bt_stride = a.block_table_stride;
@@ -1195,29 +1195,14 @@ cudaError_t launch_cache_attention(const li_cache_attn_args &a, const CacheAttnP
     P.head_blocks = p.head_blocks;
     P.by_heads = FixedDiv(p.head_blocks);
     P.tiles = p.tiles;
-    P.cuts = p.cuts;
-    P.chunk = p.chunk;
-    P.by_cuts = FixedDiv(p.cuts);
+    P.cut_log2 = p.cut_log2;
     P.slots = p.slots;
     P.p_off = p.p_off;
     P.slot_off = p.slot_off;
     P.tmem_cols = p.tmem_cols;
     // the statistics cost a maximum per score: a kernel of their own
-    cudaError_t e = p.N == 16 ? (smax ? launch_main<16, true>(P, p.grid, st)
-                                      : launch_main<16, false>(P, p.grid, st))
-                              : (smax ? launch_main<32, true>(P, p.grid, st)
-                                      : launch_main<32, false>(P, p.grid, st));
-    if (e != cudaSuccess || p.cuts == 1) return e;
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(p.units / p.cuts), (unsigned)(a.G < 32 ? a.G : 32));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = st;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel, P, p.N);
+    return p.N == 16 ? (smax ? launch_main<16, true>(P, p.grid, st) : launch_main<16, false>(P, p.grid, st))
+                     : (smax ? launch_main<32, true>(P, p.grid, st) : launch_main<32, false>(P, p.grid, st));
 }
 
 }  // namespace li

@@ -72,8 +72,7 @@ EXPORTS = ("li_metadata_workspace_size", "li_metadata", "li_indexer_workspace_si
            "li_abi_version", "li_indexer_noalloc", "li_plan", "li_merge_topk",
            "li_kl_grad_workspace_size", "li_kl_grad", "li_sparse_attention_workspace_size",
            "li_sparse_attention", "li_rope", "li_rope_grad", "li_rope_frequencies",
-           "li_cache_write", "li_cache_read", "li_cache_attention_workspace_size",
-           "li_cache_attention")
+           "li_cache_write", "li_cache_read", "li_cache_attention")
 
 MERGE_MAX_LISTS = 16          # LI_MERGE_MAX_LISTS
 
@@ -232,10 +231,9 @@ def load(path) -> ctypes.CDLL:
                                       ctypes.POINTER(ctypes.c_float)]
     L.li_cache_write.argtypes = [ctypes.POINTER(LiCacheArgs), vp]
     L.li_cache_read.argtypes = [ctypes.POINTER(LiCacheArgs), vp]
-    L.li_cache_attention_workspace_size.argtypes = [ctypes.POINTER(LiCacheAttnArgs), sz]
-    L.li_cache_attention.argtypes = [ctypes.POINTER(LiCacheAttnArgs), vp, ctypes.c_size_t, vp, vp, vp, vp]
+    L.li_cache_attention.argtypes = [ctypes.POINTER(LiCacheAttnArgs), vp, vp, vp, vp]
     for f in ("li_rope", "li_rope_grad", "li_rope_frequencies", "li_cache_write", "li_cache_read",
-              "li_cache_attention_workspace_size", "li_cache_attention"):
+              "li_cache_attention"):
         getattr(L, f).restype = ctypes.c_int
     L.li_abi_version.argtypes = []
     L.li_abi_version.restype = ctypes.c_int32
@@ -827,19 +825,16 @@ def cache_attention(q, codes, descale, sparse_indices, scale, q_rope=None, rope_
     G, Dm) bf16, or (out, softmax_max, softmax_sum) with return_stats, (B, 1, S1, G) fp32."""
     a = make_cache_attn_args(q, codes, descale, sparse_indices, scale, q_rope, rope_cache,
                              block_table, s2, device_status)
-    dev, L, n = q.device, lib(), ctypes.c_size_t(0)
+    dev = q.device
     if check and device_status is None:
         device_status = _zero_status(dev, stream)
         a.device_status = device_status.data_ptr()
-    ref = ctypes.byref(a)
-    _on_device(dev, L.li_cache_attention_workspace_size, ref, ctypes.byref(n))
-    ws = _empty(q, n.value, torch.uint8, stream) if n.value else None      # alive until the launch
     out = _empty_like(q, stream)
     smax = ssum = None
     if return_stats:
         shape = (q.shape[0], 1, q.shape[1], q.shape[2])
         smax, ssum = (_empty(q, shape, torch.float32, stream) for _ in range(2))
-    _on_device(dev, L.li_cache_attention, ref, _ptr(ws), n.value, out.data_ptr(), _ptr(smax), _ptr(ssum),
+    _on_device(dev, lib().li_cache_attention, ctypes.byref(a), out.data_ptr(), _ptr(smax), _ptr(ssum),
                _raw_stream(dev, stream))
     if check:
         _raise_on(dev, device_status, stream)

@@ -46,6 +46,11 @@ CASES = {
     "wild_scales": dict(B=2, S1=2, S2=300, G=16, Dm=128, Dr=64, topk=256, spread=6.0, q_std=0.01),
     "peaked": dict(B=2, S1=3, S2=900, G=16, Dm=512, Dr=64, topk=900, scale=0.5),
     "flat": dict(B=1, S1=2, S2=900, G=32, Dm=512, Dr=64, topk=900, q_std=1e-3),
+    # two, four and eight CTAs to a row (the single token above: eight)
+    "shared_by_two": dict(B=40, S1=1, S2=700, G=16, Dm=256, Dr=64, topk=600),
+    "shared_by_two_32": dict(B=35, S1=1, S2=700, G=24, Dm=128, Dr=0, topk=641),
+    "shared_by_four": dict(B=5, S1=4, S2=900, G=7, Dm=512, Dr=0, topk=777, block=48),
+    "shared_by_eight": dict(B=1, S1=2, S2=1200, G=32, Dm=512, Dr=64, topk=1153, pow2=False),
     "topk8192": dict(B=1, S1=2, S2=9000, G=16, Dm=128, Dr=0, topk=8192),
 }
 

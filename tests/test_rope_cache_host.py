@@ -190,30 +190,19 @@ _DENSE_ATTN = dict(layout_k=0, block_table=None, block_table_stride=0, num_block
     dict(device_status=0x60002), dict(reserved=1),
     dict(Dr=64, q_rope=0x60008, k_rope=0x70000), dict(Dr=64, q_rope=0x60000, k_rope=0x70008)])
 def test_cache_attention_refusals(L, kw):
-    n = ctypes.c_size_t(0)
-    assert L.li_cache_attention_workspace_size(ctypes.byref(_cattn(**kw)), ctypes.byref(n)) == 1, kw
-    assert L.li_cache_attention(ctypes.byref(_cattn(**kw)), 0x100000, 1 << 40, 0x200000, None, None, None) == 1
+    assert L.li_cache_attention(ctypes.byref(_cattn(**kw)), 0x200000, None, None, None) == 1, kw
     assert li.li_last_error_string()
 
 
-def test_cache_attention_outputs_workspace_and_limits(L):
-    n = ctypes.c_size_t(0)
-    size = L.li_cache_attention_workspace_size
-    # one tile of selected keys a row is never cut: no workspace; two tiles may be
-    assert size(ctypes.byref(_cattn(topk=128)), ctypes.byref(n)) == 0 and n.value == 0
-    assert size(ctypes.byref(_cattn(topk=513)), ctypes.byref(n)) == 0 and n.value % 256 == 0 and n.value > 0
-    need = n.value
-    run = lambda ws, b, out, m=None, s=None: L.li_cache_attention(ctypes.byref(_cattn(topk=513)), ws, b, out, m, s, None)  # noqa: E731
-    assert run(None, need, 0x200000) == 3 and run(0x100010, need, 0x200000) == 3
-    assert run(0x100000, need - 256, 0x200000) == 3
-    assert run(0x100000, need, None) == 1 and run(0x100000, need, 0x200008) == 1
-    assert run(0x100000, need, 0x200000, 0x300000) == 1 and run(0x100000, need, 0x200000, 0x300000, 0x400002) == 1
-    assert size(ctypes.byref(_cattn(batch=1 << 14, s1=1 << 11)), ctypes.byref(n)) == 2
-    assert size(ctypes.byref(_cattn(num_blocks=1 << 25, block_size=128)), ctypes.byref(n)) == 2
+def test_cache_attention_outputs_and_limits(L):
+    def run(out, m=None, s=None, **kw):
+        return L.li_cache_attention(ctypes.byref(_cattn(**kw)), out, m, s, None)
+    assert run(None) == 1 and run(0x200008) == 1
+    assert run(0x200000, 0x300000) == 1 and run(0x200000, 0x300000, 0x400002) == 1
+    assert run(0x200000, batch=1 << 14, s1=1 << 11) == 2
+    assert run(0x200000, num_blocks=1 << 25, block_size=128) == 2
     # every head count and size of key fits; no rows need no launch
     for G in (1, 16, 17, 32, 33, 128):
         for Dm in (128, 256, 384, 512):
             for rope in (dict(), dict(Dr=64, q_rope=0x60000, k_rope=0x70000)):
-                assert size(ctypes.byref(_cattn(G=G, Dm=Dm, **rope)), ctypes.byref(n)) == 0
-    empty = _cattn(batch=0)
-    assert L.li_cache_attention(ctypes.byref(empty), 0x100000, 1 << 30, None, None, None, None) == 0
+                assert run(None, batch=0, G=G, Dm=Dm, **rope) == 0
