@@ -177,6 +177,24 @@ def test_extreme_rows(dtype, pow2):
     assert torch.equal(got_c[~nan], want_c[~nan])
 
 
+@pytest.mark.parametrize("dim,dtype", [(16, torch.float32), (48, torch.bfloat16), (496, torch.float16),
+                                       (528, torch.bfloat16), (1008, torch.bfloat16), (1024, torch.float32)])
+def test_many_rows(dim, dtype):
+    """Enough rows that a lane takes more of each (more than eight elements a thread of the device),
+    dims that do not divide by the lanes."""
+    n = 148 * 2048 * 8 // dim + 77
+    g = torch.Generator().manual_seed(dim)
+    x = torch.randn(1, n, dim, generator=g).to(dtype)
+    x[0, :, -1] *= 9                        # the last element counts in every row's maximum
+    codes = torch.zeros(1, n, 1, dim, dtype=torch.float8_e4m3fn, device="cuda")
+    scale = torch.zeros(1, n, device="cuda")
+    li.cache_write(x.cuda(), codes, scale)
+    want, s = ref.quantise(x[0])
+    assert torch.equal(_bytes(codes).view(n, dim), want) and torch.equal(scale.cpu()[0], s)
+    back = li.cache_read(codes, scale, torch.zeros(1, n, dim, dtype=dtype, device="cuda"))[0]
+    assert torch.equal(back.cpu()[0], (codes.cpu().float().view(n, dim) * s[:, None]).to(dtype))
+
+
 def test_strided_rows():
     """x and rope as column ranges of one projection, at an aligned and an unaligned start, and rows
     of a longer batch; reading back into such views leaves the other columns alone."""
