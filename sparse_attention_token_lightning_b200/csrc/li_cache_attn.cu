@@ -520,6 +520,7 @@ __device__ void gather_role(const Params &P, uint8_t *smem, Tail *T, const Bars 
             bool there = true;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
+                if (r[i] >= 0 && !idx_ok(r[i], P.key_rows, P.status)) r[i] = -1;
                 size[i] = r[i] < 0 ? 0u : 16u;
                 r[i] = max(r[i], 0);
                 row[i] = codes + (uint64_t)(uint32_t)r[i] * (uint32_t)P.Dm;
