@@ -30,9 +30,9 @@
 //   gather    copies codes and rope part with cp.async into 16 KB slots (128 keys x 128 bytes,
 //             128-byte swizzle); rows that select nothing are zero-filled
 //   qk, pv    one thread each issues the two products
-// Measured (576 values a key, 16 heads; graph replay on one B200): 64 sequences x 2048 keys 26.4 us (85 MB
-// of selected rows, 3.2 TB/s; what memory alone takes is 13.3), one sequence 12.5, causal 2048 tokens x 1024
-// keys 171 us (1.05 GB out of L2, 6.1 TB/s), 21 rows x 777 keys x 128 heads of 256 19.5 us.
+// Measured (576 values a key, 16 heads; graph replay on one B200): 64 sequences x 2048 keys 25.6 us (85 MB
+// of selected rows, 3.3 TB/s; what memory alone takes is 13.3), one sequence 12.5, causal 2048 tokens x 1024
+// keys 168 us (1.05 GB out of L2, 6.3 TB/s), 21 rows x 777 keys x 128 heads of 256 19.5 us.
 // A tile then costs a CTA some 3700 cycles, of which no unit is full: the gather alone takes 2140 (38
 // bytes a cycle and SM, for 16 SMs as for 148), the operands of the products 150 KB of shared memory
 // (1500 cycles), a softmax from scores to weights 2000. More overlap did not help: with tiles of 64 keys
@@ -825,20 +825,27 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                     ok = ok && wait_lane(bars.p_empty(b ^ 1u), ((kt - 1) >> 1) & 1u, abort_flag);
                     __syncwarp();
                     tc_fence_after();
+                    // two reads in flight where the registers allow (2048 tokens 168 us against 171)
+                    constexpr int kB = 16 / H;
 #pragma unroll 1
-                    for (int c = 0; c < 2 * P.blocks; ++c) {        // hi and lo of each block
+                    for (int c = 0; c < 2 * P.blocks; c += kB) {    // hi and lo of each block
                         const uint32_t o = tmem + lanes + 2 * kSCols<N> + c * N + col;
-                        uint32_t x[H];
-                        tmem_ld_nowait(o, x);
+                        uint32_t x[kB][H];
+#pragma unroll
+                        for (int b = 0; b < kB; ++b) tmem_ld_nowait(o + b * N, x[b]);
                         tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < H; i += 4) {
                             float a4[4];
                             lds4(T->alpha[g] + i, a4);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) x[i + k] = __float_as_uint(__uint_as_float(x[i + k]) * a4[k]);
+                            for (int b = 0; b < kB; ++b)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    x[b][i + k] = __float_as_uint(__uint_as_float(x[b][i + k]) * a4[k]);
                         }
-                        tmem_st_nowait(o, x);
+#pragma unroll
+                        for (int b = 0; b < kB; ++b) tmem_st_nowait(o + b * N, x[b]);
                     }
                     tmem_wait_st();
                     tc_fence_before();
@@ -921,7 +928,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
         // neighbouring lanes exchange halves: an even lane stores two dims of the even heads, an odd
         // lane of the odd heads
         uint16_t *out = P.out + (head_at + (lane & 1)) * P.Dm + (key & ~1);
-#pragma unroll 1
+#pragma unroll (16 / H)
         for (int c = 0; c < P.blocks; ++c, po += 128, out += 128) {
             float o[H];
 #pragma unroll
