@@ -644,17 +644,18 @@ def rope_grad(dy, positions, freqs: RopeFrequencies, offset: int = 0, interleave
 
 
 def _rows_of(t, dims, name):
-    """Shape and strides of rows (..., D) in `dims` dimensions, a head dimension of 1 before D
-    left out: keys have one head."""
+    """(B, S, D, batch stride, row stride) of rows (B, S, D), or (T, 0, D, 0, row stride) of rows
+    (T, D), in `dims` dimensions or with a head dimension of 1 before D (keys have one head)."""
     shape, strides = t.shape, t.stride()
     n = len(shape)
-    if n == dims + 1 and shape[-2] == 1:
-        shape, strides = shape[:-2] + shape[-1:], strides[:-2] + strides[-1:]
-    elif n != dims:
+    if n != dims and (n != dims + 1 or shape[-2] != 1):
         raise ValueError(f"{name} has shape {tuple(shape)}, {dims} dimensions (or a head of 1 more) wanted")
-    if shape[-1] > 1 and strides[-1] != 1:
+    D = shape[-1]
+    if D > 1 and strides[-1] != 1:
         raise ValueError(f"the last dimension of {name} must be dense")
-    return shape, strides
+    if dims == 2:
+        return shape[0], 0, D, 0, strides[0]
+    return shape[0], shape[1], D, strides[0], strides[1]
 
 
 def _cache_ptr(t, dev, name, dtype, n0, n1, D):
@@ -678,16 +679,16 @@ def make_cache_args(x, codes, descale, rope=None, rope_cache=None, seqused_k=Non
     a = LiCacheArgs()
     tnd = cu_seqlens is not None
     dims = 2 if tnd else 3
-    shape, strides = _rows_of(x, dims, "x")
-    D, (n0, n1) = shape[-1], codes.shape[:2]
-    a.x, a.x_row_stride = x.data_ptr(), strides[-2]
+    B, S, D, a.x_batch_stride, a.x_row_stride = _rows_of(x, dims, "x")
+    lead = B, S
+    a.x = x.data_ptr()
     if tnd:
+        a.layout_x, a.x_len = 1, B
         B = cu_seqlens.shape[0] - 1
         a.cu_seqlens = _ptr_of(cu_seqlens, dev, "cu_seqlens", torch.int32, (max(B, 0) + 1,))
-        a.layout_x, a.x_len = 1, shape[0]
     else:
-        B = shape[0]
-        a.x_len, a.x_batch_stride = shape[1], strides[0]
+        a.x_len = S
+    n0, n1 = codes.shape[:2]
     a.batch, a.dim, a.dtype = B, D, dtype
     a.codes = _cache_ptr(codes, dev, "codes", torch.float8_e4m3fn, n0, n1, D)
     a.descale = _ptr_of(descale, dev, "descale", torch.float32, (n0, n1))
@@ -709,14 +710,11 @@ def make_cache_args(x, codes, descale, rope=None, rope_cache=None, seqused_k=Non
     if (rope is None) != (rope_cache is None):
         raise ValueError("rope and rope_cache go together")
     if rope is not None:
-        rows, strides = _rows_of(rope, dims, "rope")
-        R = rows[-1]
-        if rope.device != dev or rope.dtype is not kind or rows[:-1] != shape[:-1]:
-            raise ValueError(f"rope must be {kind} {tuple(shape[:-1])} + (rope_dim,) on {dev}, got "
+        n, m, R, a.rope_batch_stride, a.rope_row_stride = _rows_of(rope, dims, "rope")
+        if rope.device != dev or rope.dtype is not kind or (n, m) != lead:
+            raise ValueError(f"rope must be {kind} with the rows of x {tuple(x.shape)} on {dev}, got "
                              f"{rope.dtype} {tuple(rope.shape)} on {rope.device}")
-        a.rope, a.rope_row_stride, a.rope_dim = rope.data_ptr(), strides[-2], R
-        if not tnd:
-            a.rope_batch_stride = strides[0]
+        a.rope, a.rope_dim = rope.data_ptr(), R
         a.rope_cache = _cache_ptr(rope_cache, dev, "rope_cache", kind, n0, n1, R)
     if device_status is not None:
         a.device_status = _status_ptr(device_status, dev)
