@@ -110,13 +110,14 @@ struct Bars {
     __device__ uint32_t looked_up(int i) const { return at(15 + 2 * kTileRing + i); }   // both read
     __device__ uint32_t slot_full(int i) const { return at(15 + 3 * kTileRing + i); }
     __device__ uint32_t slot_empty(int i) const { return at(15 + 3 * kTileRing + kMaxSlots + i); }
+    __device__ uint32_t drained(int i) const { return at(15 + 3 * kTileRing + 2 * kMaxSlots + i); }
 };
-constexpr int kNumBars = 15 + 3 * kTileRing + 2 * kMaxSlots;
+constexpr int kNumBars = 17 + 3 * kTileRing + 2 * kMaxSlots;
 struct Tail {
     uint64_t bars[kNumBars];
     int32_t tiles[2];                           // the units' tiles left
     uint32_t tmem;
-    volatile int abort_flag;
+    volatile int abort_flag, no_abort;          // no_abort: always 0
     alignas(16) int vote[2][2][4];              // [group][turn][warp]
     alignas(16) float ah[kAhRing][32];          // scale log2(e) / the head's power of two
     alignas(16) float ref[2][16];               // [group][head]: y of a weight 1
@@ -494,6 +495,9 @@ __device__ void prep_role(const Params &P, uint8_t *smem, Tail *T, const Bars &b
 // ---- gather ----------------------------------------------------------------------------------------
 template <int N>
 __device__ void gather_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bars) {
+#if defined(LI_TEST_NO_LOADS)
+    return;     // test build: no copy and no arrival, so that the first product's wait runs out
+#endif
     const int w = (threadIdx.x >> 5) - Roles<N>::kGather0, lane = threadIdx.x & 31;
     const int piece = lane & 7, sub = lane >> 3;        // this lane copies keys 32 w + sub + 4 i
     const uint8_t *codes = P.codes + piece * 16, *ropes = reinterpret_cast<const uint8_t *>(P.k_rope) + piece * 16;
@@ -552,6 +556,16 @@ __device__ void gather_role(const Params &P, uint8_t *smem, Tail *T, const Bars 
     }
     asm volatile("cp.async.wait_all;" ::: "memory");    // no copy may outlive the CTA
     if (!ok) T->abort_flag = 1;
+}
+
+// A warp that issues products gives up: those under way still read shared memory and write TMEM, so
+// it waits for them, with the limit of every wait.
+__device__ __noinline__ void drain(Tail *T, uint32_t bar) {
+    T->abort_flag = 1;
+    if (elect_one()) umma_commit(bar);
+    __syncwarp();
+    wait_long(bar, 0, &T->no_abort);
+    __syncwarp();
 }
 
 // ---- products --------------------------------------------------------------------------------------
@@ -619,7 +633,7 @@ __device__ void qk_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
         __syncwarp();
         ++nu;
     }
-    T->abort_flag = 1;
+    drain(T, bars.drained(0));
 }
 
 template <int N>
@@ -664,7 +678,7 @@ __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
         if (!ok) break;
         ++nu;
     }
-    T->abort_flag = 1;
+    drain(T, bars.drained(1));
 }
 
 // A share's partial outputs in shared memory, from slot_off on: O [N][Dm] in fp32, then per head its
@@ -1043,6 +1057,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const
             mbar_init(bars.s_empty(i), R::kSoft);
             mbar_init(bars.p_full(i), 32 * R::kSoft);
             mbar_init(bars.p_empty(i), 1);
+            mbar_init(bars.drained(i), 1);
         }
         mbar_init(bars.q_full(), 32 * R::kPrep);
         mbar_init(bars.q_empty(), 1);
@@ -1056,7 +1071,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const
             mbar_init(bars.slot_full(i), 32 * kGatherWarps);
             mbar_init(bars.slot_empty(i), 1);
         }
-        T->abort_flag = 0;
+        T->abort_flag = T->no_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == R::kQk) {

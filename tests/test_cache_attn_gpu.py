@@ -3,12 +3,13 @@ in cache_attn_ref from the kernel's arithmetic."""
 import os
 import subprocess
 import sys
+import time
 
 import pytest
 import torch
 
 import cache_attn_ref as ref
-from sparse_attention_token_lightning_b200 import li
+from sparse_attention_token_lightning_b200 import build, li
 
 pytestmark = pytest.mark.gpu
 
@@ -199,6 +200,22 @@ def test_reruns_graphs_and_streams_are_bit_identical():
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(a, o)
+
+
+@pytest.mark.parametrize("name", ["single_token", "shared_by_two", "causal", "heads128"])
+def test_a_wait_that_runs_out_is_reported(monkeypatch, name):
+    """The test build gives up a wait after 1 ms and gathers nothing: the first product's wait runs out,
+    every role leaves, the CTAs of a cluster still meet, and the call reports it. The context stays
+    usable: the library's own call gives the same bits as before."""
+    p = ref.make(seed=len(name), **CASES[name])
+    before = run(p)
+    monkeypatch.setattr(li, "_lib", li.load(build.build_wait_test()))
+    t0 = time.perf_counter()
+    with pytest.raises(li.LiError) as e:
+        run(p)
+    assert e.value.status == 5 and time.perf_counter() - t0 < 20.0       # LI_ERR_DEVICE_TIMEOUT
+    monkeypatch.undo()
+    assert all(torch.equal(a, b) for a, b in zip(before, run(p)))
 
 
 FIRST_CALL = """
