@@ -12,7 +12,8 @@
 //   weights with y = x log2(e) + log2(d_s), 2^(y - ref) = hi + lo / 16 likewise (9 bits by way of
 //           fp16's 11: 1.25 x 2^-9, less than a bf16 weight's 2^-8). The reference follows the
 //           largest y, not the largest x, so the scale is inside the exponent and the parts are
-//           full where the products are large; the normaliser sums 2^(y - ref) / d_s in fp32.
+//           full where the products are large; the normaliser sums 2^(x log2(e) - ref) in fp32, whose
+//           largest terms are normal numbers for every scale in [2^-100, 2^100].
 // The products S = K Q^T (keys on M = 128, hi and lo heads on N) and O^T += V^T P^T (dims on M = 128,
 // the key tile read MN-major, keys on K) both read the same gathered tile; the rope part is a bf16
 // product of its own into other TMEM columns, since its codes have no scale.
@@ -122,7 +123,7 @@ struct Tail {
     alignas(16) float ah[kAhRing][32];          // scale log2(e) / the head's power of two
     alignas(16) float ref[2][16];               // [group][head]: y of a weight 1
     alignas(16) float coef[2][16];              // what O counts in the output
-    alignas(16) float alpha[2][16], moved[2][16];
+    alignas(16) float alpha[2][16], moved[2][16];   // root of what O and the sums shrink by; its log2
     int seen[2][16], fresh[2];                  // whether a head's reference is set; any that is not
     alignas(16) float red[2][16][4];            // [group][head][warp]
     alignas(16) float lsum[2][16][4], mx[2][16][4];
@@ -754,7 +755,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.looked_up(tr));
-            const float log2d = log2f(d), inv_d = d > 0.0f ? __frcp_rn(d) : 0.0f;
+            const float log2d = log2f(d), back = d > 0.0f ? log2d : 0.0f;
             ok = ok && wait_lane(bars.s_full(b), (kt >> 1) & 1u, abort_flag);
             float t[H];                                 // y - ref, the weights' exponents
             __syncwarp();
@@ -816,7 +817,9 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                     const bool seen = T->seen[g][lane] != 0;
                     const float up = seen ? fmaxf(most - kShift, 0.0f) : most > -kInf ? most - kShift : 0.0f;
                     T->ref[g][lane] += up;
-                    T->alpha[g][lane] = seen ? exp2_(-up) : 0.0f;   // nothing is summed before the first
+                    // nothing is summed before the first. The root: 2^-up itself may underflow where a
+                    // key with a small scale has its share of the sums
+                    T->alpha[g][lane] = seen ? exp2_(-0.5f * up) : 0.0f;
                     T->moved[g][lane] = up;
                     T->seen[g][lane] = seen || most > -kInf;
                     const bool all_seen = __all_sync((1u << H) - 1u, seen || most > -kInf);
@@ -831,7 +834,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                     lds4(T->moved[g] + i, u4);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        l[i + k] *= a4[k];
+                        l[i + k] = l[i + k] * a4[k] * a4[k];
                         t[i + k] -= u4[k];
                     }
                 }
@@ -856,7 +859,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                             for (int b = 0; b < kB; ++b)
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
-                                    x[b][i + k] = __float_as_uint(__uint_as_float(x[b][i + k]) * a4[k]);
+                                    x[b][i + k] = __float_as_uint(__uint_as_float(x[b][i + k]) * (a4[k] * a4[k]));
                         }
 #pragma unroll
                         for (int b = 0; b < kB; ++b) tmem_st_nowait(o + b * N, x[b]);
@@ -874,8 +877,10 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
 #pragma unroll
             for (int i = 0; i < H; i += 2) {
                 const float p0 = exp2_(t[i]), p1 = exp2_(t[i + 1]);
-                l[i] = fmaf(p0, inv_d, l[i]);
-                l[i + 1] = fmaf(p1, inv_d, l[i + 1]);
+                // e^x / 2^ref: an exponential of its own, since 2^(y - ref) may underflow where the scales
+                // span more than 2^126 and this does not
+                l[i] += exp2_(t[i] - back);
+                l[i + 1] += exp2_(t[i + 1] - back);
                 uint32_t h8, l8;
                 split_e4m3(__floats2half2_rn(p0, p1), &h8, &l8);
                 if (i & 2) {
@@ -1019,8 +1024,9 @@ __device__ void join(const Params &P, uint8_t *smem) {
             // a share without keys left no outputs: not even a NaN of what lies there may count
             if (i >= cuts) break;
             if (l[i] == 0.0f) continue;
-            w[i] = exp2_(w[i] - most);
-            sum = fmaf(l[i], w[i], sum);
+            const float root = exp2_(0.5f * (w[i] - most));     // as where a reference moves
+            w[i] = root * root;
+            sum = fmaf(l[i] * root, root, sum);
             o.x = fmaf(v[i].x, w[i], o.x);
             o.y = fmaf(v[i].y, w[i], o.y);
             o.z = fmaf(v[i].z, w[i], o.z);
