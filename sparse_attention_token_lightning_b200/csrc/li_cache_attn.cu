@@ -22,9 +22,9 @@
 // keys. When there are few rows (decode) a cluster of two, four or eight CTAs shares each unit's tiles,
 // and joins its partial outputs through distributed shared memory (cache_attn_plan says when). Warps:
 //   softmax   two groups of 4 warps, each with half the heads: a thread owns one key of the tile and
-//             8 or 16 heads. The largest weight is set to 2^4 and may grow to 2^8 (E4M3 holds 448)
+//             8 or 16 heads. The largest weight is set to 2^7 and may grow to 2^8.75 (E4M3 holds 448)
 //             before the reference moves; a vote per tile finds that out, and only then are the
-//             maxima reduced and O rescaled. Weights below 2^-18 of the largest may round to 0
+//             maxima reduced and O rescaled. Weights below 2^-21 of the largest may round to 0
 //   prep      the next unit's q: normalised, split and stored in the MMA layout
 //   lookup    each selected key's cache row for the gather and its scale for the softmax warps, a few
 //             tiles ahead, and how many tiles a unit has
@@ -69,8 +69,12 @@ constexpr uint32_t kTailBytes = 8192;
 constexpr uint32_t kTailOff = kSmemBytes - kTailBytes;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // A tile's largest weight is set to 2^kShift when the reference moves, and it moves when a weight
-// would pass 2^kTop (of the 448 that E4M3 holds).
-constexpr float kShift = 4.0f, kTop = 8.0f;
+// would pass 2^kTop (of the 448 that E4M3 holds). The lo part ends in steps of 2^-13, so a weight is held
+// to 2^-(14 + kShift) of the row's largest, and what a sink's tail of n keys may lose in all is n times
+// that: 2^-10 of the output at 2048 keys and 2^-8, half a step of bf16, at 8192. More room for fewer
+// moves takes accuracy: 2048 tokens took 169 us with a shift of 4 (up to 2^-5 there), 174 with 6, 178 with 7
+// and 184 with 8.
+constexpr float kShift = 7.0f, kTop = 8.75f;
 constexpr uint32_t kNoKey = 0xffc0ffeeu;            // a NaN that marks it
 constexpr float kNoRef = -1e30f;                    // reference of a piece without keys
 constexpr float kMinDescale = 7.888609052210118e-31f, kMaxDescale = 1.2676506002282294e30f;  // 2^+-100

@@ -12,7 +12,7 @@ from sparse_attention_token_lightning_b200 import li
 
 pytestmark = pytest.mark.gpu
 
-FLOOR = 2.0 ** -18      # half of the lo part's last step where the largest weight is at least 2^4
+FLOOR = 2.0 ** -21      # half of the lo part's last step, 2^-14, where the largest weight is at least 2^7
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -97,3 +97,22 @@ def test_scales_of_every_size(rows, topk):
     some = slice(None, None, 1 + rows // 8)
     got = attend(idx, codes, descale, k_rope, q_rope, scale=0.125)
     check([t[some] for t in got], idx[some], codes, descale, k_rope, q_rope[some], scale=0.125)
+
+
+@pytest.mark.parametrize("rows", [1, 100])
+@pytest.mark.parametrize("n", [2048, 8192])
+@pytest.mark.parametrize("sink", [0, 777, 2047])
+def test_a_sink_with_a_long_tail(rows, n, sink):
+    """One key takes nearly all of the weight, and thousands of others, each too small to count, have values
+    where it has none: what they are worth together arrives, to n FLOOR. The tail's weights are e^-10 ...
+    e^-17.5 (2^-14 ... 2^-25) of the sink's, by head; shared by eight CTAs (one row) or not (100)."""
+    codes, descale = torch.zeros(n, 128), torch.ones(n)
+    codes[:, 64:], k_rope = 448.0, torch.zeros(n, 64)
+    k_rope[:, 0] = -1
+    codes[sink] = torch.cat([torch.full((64,), 448.0), torch.zeros(64)])
+    k_rope[sink] = 0
+    q_rope = torch.zeros(rows, 16, 64)
+    q_rope[:, :, 0] = 10 + 0.5 * torch.arange(16)
+    idx = torch.arange(n).expand(rows, n).contiguous()
+    got = attend(idx, codes, descale, k_rope, q_rope)
+    check([t[::33] for t in got], idx[::33], codes, descale, k_rope, q_rope[::33])
