@@ -40,6 +40,11 @@ def headers():
 WAIT_TEST_LIB = PKG / "libli_waittest.so"
 WAIT_TEST_FLAGS = ("-DLI_WAIT_LIMIT_NS=1000000ull", "-DLI_TEST_NO_LOADS=1")
 
+# Test build: the same limit, and the cache attention announces no unit's last value product, so that the
+# wait before the output runs out (the product itself ends long before).
+LAST_WAIT_TEST_LIB = PKG / "libli_lastwaittest.so"
+LAST_WAIT_TEST_FLAGS = ("-DLI_WAIT_LIMIT_NS=1000000ull", "-DLI_TEST_NO_LAST_COMMIT=1")
+
 
 # Bounds-checked build: every computed shared- or global-memory index the kernels form passes a
 # check first; a failing check sets LI_DEVERR_BOUNDS in the status word and the access is
@@ -59,6 +64,11 @@ def up_to_date(lib: Path = LIB) -> bool:
 def build_wait_test(force: bool = False, verbose: bool = False) -> Path:
     """libli_waittest.so (see WAIT_TEST_FLAGS)."""
     return build(force, verbose, WAIT_TEST_FLAGS, lib=WAIT_TEST_LIB, obj_sub="waittest")
+
+
+def build_last_wait_test(force: bool = False, verbose: bool = False) -> Path:
+    """libli_lastwaittest.so (see LAST_WAIT_TEST_FLAGS)."""
+    return build(force, verbose, LAST_WAIT_TEST_FLAGS, lib=LAST_WAIT_TEST_LIB, obj_sub="lastwaittest")
 
 
 def build_debug(force: bool = False, verbose: bool = False) -> Path:
@@ -102,5 +112,6 @@ def build(force: bool = False, verbose: bool = False, extra=(), lib: Path = LIB,
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose="-v" in sys.argv)
     build_wait_test(force="--force" in sys.argv, verbose="-v" in sys.argv)
+    build_last_wait_test(force="--force" in sys.argv, verbose="-v" in sys.argv)
     build_debug(force="--force" in sys.argv, verbose="-v" in sys.argv)
     print(LIB)

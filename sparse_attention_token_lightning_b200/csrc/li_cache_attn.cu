@@ -675,7 +675,11 @@ __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
                     umma_commit(bars.slot_empty(slot));
                     if (++slot == P.slots) slot = 0;
                 }
-                umma_commit(bars.p_empty(kt & 1u));
+#if defined(LI_TEST_NO_LAST_COMMIT)
+                // test build: a unit's last product is not announced, so that the output's wait runs out
+                if (j < tiles - 1)
+#endif
+                    umma_commit(bars.p_empty(kt & 1u));
             }
             __syncwarp();
             sr.next(P.slots, P.has_rope + P.blocks);
@@ -916,13 +920,21 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 T->lsum[g][held][q] = ws;
                 if (kStats) T->mx[g][held][q] = wm;
             }
-            ok = ok && wait_lane(bars.p_empty((kt - 1) & 1u), ((kt - 1) >> 1) & 1u, abort_flag);
+            const uint32_t last = bars.p_empty((kt - 1) & 1u), parity = ((kt - 1) >> 1) & 1u;
+            ok = ok && wait_lane(last, parity, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+                // no vote follows the last unit, so the flag is set here and the warp stores nothing. The warp
+                // that issued the product may have left: wait once more before what it works on is given back
+                *abort_flag = 1;
+                wait_long(last, parity, &T->no_abort);
+            }
             __syncwarp();
             named_bar(bar_id, 128);
         }
         const int heads = min(P.G - u.head0 - col, H);          // may be <= 0
         const int64_t head_at = (int64_t)u.row * P.G + u.head0 + col;
-        const bool row_ok = idx_ok(u.row, P.rows, P.status);
+        const bool row_ok = ok && idx_ok(u.row, P.rows, P.status);
         if (q == 0 && lane < H) {
             float r = kNoRef, s = 0.0f, m = -kInf;
             if (tiles > 0) {
