@@ -695,6 +695,12 @@ __device__ void pv_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bar
 template <int N> __device__ __forceinline__ uint32_t part_stat(int32_t Dm, int h) { return (uint32_t)(N * Dm + 4 * h) * 4u; }
 
 // ---- softmax and output ------------------------------------------------------------------------------
+// Barrier of a softmax group's four warps. Its threads do different things before most of them, and the
+// aligned barrier wants a warp together; so do the TMEM reads that follow.
+__device__ __forceinline__ void group_bar(int id) {
+    __syncwarp();
+    named_bar(id, 128);
+}
 // Four consecutive floats of shared memory.
 __device__ __forceinline__ void lds4(const float *p, float (&v)[4]) {
     const float4 t = *reinterpret_cast<const float4 *>(p);
@@ -733,7 +739,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
             T->ref[g][lane] = 0.0f;
             T->seen[g][lane] = 0;
         }
-        named_bar(bar_id, 128);
+        group_bar(bar_id);
         {
             const int4 v = *reinterpret_cast<const int4 *>(T->vote[g][turn++ & 1]);
             if ((v.x | v.y | v.z | v.w) & 2) break;
@@ -805,7 +811,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
             const bool any = __any_sync(0xffffffffu, top > kTop || (fresh && d > 0.0f));
             const bool all = __all_sync(0xffffffffu, ok);
             if (lane == 0) T->vote[g][turn & 1][q] = (any ? 1 : 0) | (all ? 0 : 2);
-            named_bar(bar_id, 128);
+            group_bar(bar_id);
             const int4 v4 = *reinterpret_cast<const int4 *>(T->vote[g][turn++ & 1]);
             const int v = v4.x | v4.y | v4.z | v4.w;
             if (v & 2) {
@@ -817,7 +823,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 // first one so whatever its largest weight is; O and the sums follow
                 const float m = transpose_reduce<true>(t, lane);
                 if (holds) T->red[g][held][q] = m;
-                named_bar(bar_id, 128);
+                group_bar(bar_id);
                 if (q == 0 && lane < H) {
                     float m4[4];
                     lds4(T->red[g][lane], m4);
@@ -833,7 +839,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                     const bool all_seen = __all_sync((1u << H) - 1u, seen || most > -kInf);
                     if (lane == 0) T->fresh[g] = !all_seen;
                 }
-                named_bar(bar_id, 128);
+                group_bar(bar_id);
                 fresh = T->fresh[g] != 0;
 #pragma unroll
                 for (int i = 0; i < H; i += 4) {
@@ -929,8 +935,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 *abort_flag = 1;
                 wait_long(last, parity, &T->no_abort);
             }
-            __syncwarp();
-            named_bar(bar_id, 128);
+            group_bar(bar_id);
         }
         const int heads = min(P.G - u.head0 - col, H);          // may be <= 0
         const int64_t head_at = (int64_t)u.row * P.G + u.head0 + col;
@@ -955,7 +960,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                 P.ssum[head_at + lane] = m > -kInf ? s * exp2_(r - m) : s;
             }
         }
-        named_bar(bar_id, 128);
+        group_bar(bar_id);
         tc_fence_after();
         // O out of TMEM: a share of a unit as it is in fp32 to where its keys were (the CTA has no other
         // unit, and the last product has read them), whole units normalised as bf16
@@ -970,6 +975,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
             for (int i = 0; i < H; ++i) o[i] = 0.0f;
             if (tiles > 0) {
                 uint32_t hi[H], lo[H];
+                __syncwarp();
                 const uint32_t at = tmem + lanes + 2 * kSCols<N> + c * 2 * N + col;
                 tmem_ld_nowait(at, hi);
                 tmem_ld_nowait(at + N, lo);
@@ -1005,7 +1011,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
             }
         }
         if (tiles > 0) ++nu;
-        named_bar(bar_id, 128);         // sums, maxima and references are read before they are reset
+        group_bar(bar_id);          // sums, maxima and references are read before they are reset
     }
     T->abort_flag = 1;
 }
@@ -1100,6 +1106,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const
         tmem_alloc(smem_u32(&T->tmem), P.tmem_cols);
         tmem_relinquish();
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1119,6 +1126,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const
         pv_role<N>(P, smem, T, bars, tmem);
     }
 
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && T->abort_flag && P.status) atomicOr(P.status, LI_DEVERR_TIMEOUT);
