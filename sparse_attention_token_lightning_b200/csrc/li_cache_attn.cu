@@ -392,7 +392,10 @@ __device__ void lookup_role(const Params &P, Tail *T, const Bars &bars) {
                 else *d = __uint_as_float(kNoKey);
             }
             mbar_arrive(bars.rows_full(tr.idx));
+            // the copies arrive by themselves; the marks above are ordinary stores and take an arrival that
+            // releases them
             cp_async_arrive(bars.scales_full(tr.idx));
+            mbar_arrive(bars.scales_full(tr.idx));
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");    // no copy may outlive the CTA
@@ -1092,7 +1095,7 @@ __global__ void __launch_bounds__(Roles<N>::kThreads, 1) cache_attn_kernel(const
         mbar_init(bars.o_empty(), R::kSoft);
         for (int i = 0; i < kTileRing; ++i) {
             mbar_init(bars.rows_full(i), 32);
-            mbar_init(bars.scales_full(i), 32);
+            mbar_init(bars.scales_full(i), 2 * 32);
             mbar_init(bars.looked_up(i), kGatherWarps + R::kSoft);
         }
         for (int i = 0; i < kMaxSlots; ++i) {

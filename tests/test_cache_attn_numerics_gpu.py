@@ -116,3 +116,24 @@ def test_a_sink_with_a_long_tail(rows, n, sink):
     idx = torch.arange(n).expand(rows, n).contiguous()
     got = attend(idx, codes, descale, k_rope, q_rope)
     check([t[::33] for t in got], idx[::33], codes, descale, k_rope, q_rope[::33])
+
+
+@pytest.mark.parametrize("rows,topk", [(2, 2048), (170, 1536)])
+def test_holes_where_keys_were(rows, topk):
+    """Entries that select nothing in the places where a tile four tiles earlier (the lookups' ring) had keys
+    that outweigh all others: a mark that arrived late would give them weight. Whole tiles, halves and single
+    entries of every tile in turn."""
+    g = torch.Generator().manual_seed(topk)
+    S2 = 2100
+    codes, descale = _codes(S2, 128, g), torch.exp2(torch.randint(-3, 4, (S2,), generator=g).float())
+    k_rope, q_rope = torch.randn(S2, 64, generator=g), torch.randn(rows, 16, 64, generator=g)
+    idx = torch.stack([torch.randperm(S2, generator=g)[:topk] for _ in range(rows)])
+    tile, lane = torch.arange(topk) // 128, torch.arange(topk) % 128
+    hole = torch.where(tile % 8 < 4, torch.zeros(topk, dtype=torch.bool),
+                       torch.where(tile % 4 == 0, torch.ones(topk, dtype=torch.bool), (lane + tile) % 2 == 0))
+    idx[:, hole] = -1
+    some = slice(None, None, 1 + rows // 8)
+    first = attend(idx, codes, descale, k_rope, q_rope, scale=0.2)
+    check([t[some] for t in first], idx[some], codes, descale, k_rope, q_rope[some], scale=0.2)
+    for _ in range(20):
+        assert all(torch.equal(a, b) for a, b in zip(first, attend(idx, codes, descale, k_rope, q_rope, scale=0.2)))
