@@ -513,8 +513,10 @@ li_status li_rope_frequencies(const li_rope_scaling *scaling, double *freq, floa
  * Rows past rows_b (and TND rows behind the last sequence) are left as they are, in the cache and
  * in x. Two rows written to one cache row (a block that appears twice) leave it unspecified.
  *   device_status  uint32 or NULL: LI_DEVERR_LENGTHS is OR-ed in for lengths that do not fit (the
- *                positions outside the sequence are skipped), LI_DEVERR_TABLE for a block-table
- *                entry outside [0, num_blocks) (the row is skipped). Read it with
+ *                positions outside the sequence are skipped) and for cu_seqlens that decrease, start
+ *                below 0 or end behind x_len (rows may then go to other places of their tables'
+ *                blocks, or come from them); LI_DEVERR_TABLE for a block-table entry outside
+ *                [0, num_blocks) (the row is skipped). Read it with
  *                li_check_status(device_status, stream, &bits).
  * Limits: dim a multiple of 16 in [16, 1024], rope_dim a multiple of 8 in [0, 256], block_size in
  * [1, 1024], at most 2^31-1 rows and cache rows; codes 16-byte aligned, descale and indices

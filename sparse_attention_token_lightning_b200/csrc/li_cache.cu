@@ -43,6 +43,19 @@ __device__ __forceinline__ void report(const CacheParams &P, uint32_t bits) {
     if (bits && P.status) atomicOr(P.status, bits);
 }
 
+// Packed rows: the last block has none of them and checks the sequences' ends instead, since a row's search
+// sees only some of them. True in that block.
+__device__ __forceinline__ bool checks_sequences(const CacheParams &P) {
+    if (!P.cu_seqlens || blockIdx.x + 1 < gridDim.x) return false;
+    uint32_t err = 0;
+    for (int32_t b = threadIdx.x; b < P.batch; b += kThreads) {
+        const int32_t c0 = __ldg(P.cu_seqlens + b), c1 = __ldg(P.cu_seqlens + b + 1);
+        if (c0 < 0 || c1 < c0 || c1 > P.rows) err |= LI_DEVERR_LENGTHS;
+    }
+    report(P, err);
+    return true;
+}
+
 // Element offset of row r of the call in x (or rope), by its strides.
 __device__ __forceinline__ int64_t row_offset(const CacheParams &P, int32_t r, int64_t batch, int64_t row) {
     if (P.cu_seqlens) return (int64_t)r * row;
@@ -83,7 +96,7 @@ __device__ __forceinline__ int64_t cache_row(const CacheParams &P, int32_t r, in
         const int32_t first = __ldg(cu + b);
         i = r - first;
         L1 = __ldg(cu + b + 1) - first;
-        if (i < 0 || i >= L1) {                 // only lengths that decrease lead here
+        if (i < 0 || i >= L1) {                 // only ends that decrease lead here
             *err |= LI_DEVERR_LENGTHS;
             return -1;
         }
@@ -211,6 +224,7 @@ __device__ __forceinline__ float group_max(float m, int lanes) {
 // kSteps). The row is read before its place in the cache is looked up.
 template <class T, bool kWide, bool kPow2, int kSteps>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ CacheParams P) {
+    if (checks_sequences(P)) return;
     const int lane = threadIdx.x & (P.lanes - 1);
     const int64_t r = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> P.lanes_log2;
     Eight<T> v[kSteps], rp;
@@ -276,6 +290,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
 
 template <class T, bool kWide, int kSteps>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheParams P) {
+    if (checks_sequences(P)) return;
     const int lane = threadIdx.x & (P.lanes - 1);
     const int64_t r = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> P.lanes_log2;
     int32_t lo = 0, hi = 0;
@@ -370,7 +385,7 @@ bool wide_rows(const li_cache_args &a) {
 }
 
 unsigned blocks_of(const CacheParams &P) {
-    return (unsigned)(((int64_t)P.rows * P.lanes + kThreads - 1) / kThreads);
+    return (unsigned)(((int64_t)P.rows * P.lanes + kThreads - 1) / kThreads + (P.cu_seqlens ? 1 : 0));
 }
 
 template <class T, bool kWide, bool kPow2>
