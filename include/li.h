@@ -562,8 +562,9 @@ li_status li_cache_read(const li_cache_args *args, void *stream);
  * [2^-100, 2^100] LI_DEVERR_DESCALE (OR-ed into device_status, a uint32 or NULL; read it with
  * li_check_status(device_status, stream, &bits)).
  * Outputs: out bf16 (B,S1,G,Dm); softmax_max and softmax_sum fp32 (B,1,S1,G), both or neither NULL.
- * A row that selects no key gets out = 0, softmax_max = -inf, softmax_sum = 0. A NaN code in a
- * selected key makes the row's outputs NaN; keys that are not selected are never read.
+ * A row that selects no key gets out = 0, softmax_max = -inf, softmax_sum = 0. A NaN code or rope
+ * element of a selected key makes the row's outputs NaN, all three; a NaN in a head of q or q_rope or
+ * an infinity in one of q makes that head's NaN. Keys that are not selected are never read.
  * Limits: G in [1, 128], Dm in {128, 256, 384, 512}, Dr in {0, 64}, topk in [1, 8192], S2 >= 1
  * when there are rows, scale positive and finite; q, q_rope, codes, k_rope 16-byte aligned, the
  * rest to their elements.

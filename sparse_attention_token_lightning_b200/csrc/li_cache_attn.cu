@@ -710,6 +710,14 @@ __device__ __forceinline__ void lds4(const float *p, float (&v)[4]) {
     v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
 }
 
+// Maximum and sum of a head from its largest x log2(e), the sum against its reference, and that. Maxima leave
+// NaN out and the sum does not: a NaN there is the maximum's too.
+__device__ __forceinline__ void store_stats(const Params &P, int64_t at, float m, float sum, float ref) {
+    const float kInf = __int_as_float(0x7f800000);
+    P.smax[at] = sum != sum ? sum : m > -kInf ? m * kLn2 : m;
+    P.ssum[at] = m > -kInf ? sum * exp2_(ref - m) : sum;
+}
+
 template <int N, bool kStats>
 __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars &bars, uint32_t tmem) {
     constexpr int H = Roles<N>::kHeads;
@@ -959,8 +967,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
             if (P.cut_log2) {
                 *reinterpret_cast<float4 *>(smem + P.slot_off + part_stat<N>(P.Dm, col + lane)) = make_float4(r, s, m, 0.0f);
             } else if (kStats && lane < heads && row_ok) {
-                P.smax[head_at + lane] = m > -kInf ? m * kLn2 : m;
-                P.ssum[head_at + lane] = m > -kInf ? s * exp2_(r - m) : s;
+                store_stats(P, head_at + lane, m, s, r);
             }
         }
         group_bar(bar_id);
@@ -1063,8 +1070,7 @@ __device__ void join(const Params &P, uint8_t *smem) {
         *reinterpret_cast<uint2 *>(P.out + at * P.Dm + d) =
             make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
         if (kStats && d == 0) {
-            P.smax[at] = m > -kInf ? m * kLn2 : m;
-            P.ssum[at] = m > -kInf ? sum * exp2_(most - m) : sum;
+            store_stats(P, at, m, sum, most);
         }
     }
 }

@@ -137,3 +137,36 @@ def test_holes_where_keys_were(rows, topk):
     check([t[some] for t in first], idx[some], codes, descale, k_rope, q_rope[some], scale=0.2)
     for _ in range(20):
         assert all(torch.equal(a, b) for a, b in zip(first, attend(idx, codes, descale, k_rope, q_rope, scale=0.2)))
+
+
+@pytest.mark.parametrize("G,topk,S1", [(16, 300, 3), (40, 300, 3), (16, 2048, 1), (40, 1500, 1)])
+@pytest.mark.parametrize("what", ["code", "k_rope", "q nan", "q inf", "q -inf", "q_rope"])
+def test_not_a_number_in_all_three_outputs(G, topk, S1, what):
+    """A NaN of a key is a NaN of its rows' outputs, maximum and sum, one of a head of q (or an infinity there) of
+    that head's; other rows and heads keep their bits. Uncut rows and rows cut between CTAs."""
+    g = torch.Generator().manual_seed(G + topk)
+    S2, D = topk + 50, 128
+    codes = _codes(S2, D, g).to(torch.float8_e4m3fn).view(1, S2, 1, D)
+    kr = torch.randn(1, S2, 1, 64, generator=g).to(torch.bfloat16)
+    q, qr = (torch.randn(1, S1, G, d, generator=g).to(torch.bfloat16) for d in (D, 64))
+    idx = torch.stack([torch.randperm(S2 - 1, generator=g)[:topk] for _ in range(S1)]).view(1, S1, 1, topk).int()
+    idx[0, 0, 0, topk // 2] = S2 - 1                # a key that row 0 alone selects
+
+    def run():
+        out = li.cache_attention(q.cuda(), codes.cuda(), torch.ones(1, S2, device="cuda"), idx.cuda(), 0.05,
+                                 q_rope=qr.cuda(), rope_cache=kr.cuda(), return_stats=True)
+        return [t.cpu() for t in (out[0][0], out[1][0, 0], out[2][0, 0])]
+    clean = run()
+    hit = torch.zeros(S1, G, dtype=torch.bool)
+    if what in ("code", "k_rope"):
+        hit[0] = True
+        if what == "code":
+            codes.view(torch.uint8)[0, S2 - 1, 0, 77] = 255
+        else:
+            kr[0, S2 - 1, 0, 13] = float("nan")
+    else:
+        hit[S1 - 1, G - 3] = True
+        (qr if what == "q_rope" else q)[0, S1 - 1, G - 3, 5] = float(what.split()[-1] if what != "q_rope" else "nan")
+    for a, b in zip(clean, run()):
+        assert torch.isfinite(a).all()
+        assert torch.isnan(b[hit]).all() and torch.equal(a[~hit], b[~hit])
