@@ -167,7 +167,7 @@ li_status validate_cache_attn(const li_cache_attn_args *a, li::CacheAttnPlan *p)
         return fail(LI_ERR_UNSUPPORTED, "more than 2^24-1 query rows or 2^31-1 key rows");
     if (rows > 0 && (!a->q || !a->codes || !a->descale || !a->sparse_indices))
         return fail(LI_ERR_INVALID_ARG, "q, codes, descale and sparse_indices are required");
-    if ((a->Dr > 0) != (a->q_rope != nullptr) || (a->Dr > 0) != (a->k_rope != nullptr))
+    if (rows > 0 && ((a->Dr > 0) != (a->q_rope != nullptr) || (a->Dr > 0) != (a->k_rope != nullptr)))
         return fail(LI_ERR_INVALID_ARG, "q_rope and k_rope go with Dr > 0, and only with it");
     if (a->layout_k == LI_LAYOUT_PA_BSND) {
         if (a->block_size < 1 || a->block_size > 1024)

@@ -1,0 +1,29 @@
+"""Calls of the rotation, cache and cache attention that their documentation allows, at its edges."""
+import pytest
+import torch
+
+from sparse_attention_token_lightning_b200 import li
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    li.lib()
+
+
+def zeros(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype, device="cuda")
+
+
+@pytest.mark.parametrize("B,S1,paged", [(0, 3, False), (2, 0, False), (0, 3, True), (2, 0, True)])
+def test_attention_without_rows_and_with_a_rope_part(B, S1, paged):
+    n = 5 if paged else B
+    kw = dict(block_table=zeros(B, 2, dtype=torch.int32)) if paged else {}
+    bf = torch.bfloat16
+    out = li.cache_attention(zeros(B, S1, 16, 128, dtype=bf), zeros(n, 9, 1, 128, dtype=torch.float8_e4m3fn), zeros(n, 9),
+                             zeros(B, S1, 1, 4, dtype=torch.int32), 0.1, q_rope=zeros(B, S1, 16, 64, dtype=bf),
+                             rope_cache=zeros(n, 9, 1, 64, dtype=bf), return_stats=True, **kw)
+    assert [t.shape for t in out] == [(B, S1, 16, 128), (B, 1, S1, 16), (B, 1, S1, 16)]
