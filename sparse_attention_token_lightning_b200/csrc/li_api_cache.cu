@@ -21,6 +21,13 @@ bool strides_ok(std::initializer_list<int64_t> v) {
     return true;
 }
 
+// Whether n x m runs of d elements lie apart, at strides ns and ms: the m inside the n or the n inside the m.
+bool apart(int64_t n, int64_t ns, int64_t m, int64_t ms, int64_t d) {
+    const bool m_in = (m == 1 || ms >= d) && (n == 1 || ns >= (m == 1 ? 0 : (m - 1) * ms) + d);
+    const bool n_in = (n == 1 || ns >= d) && (m == 1 || ms >= (n == 1 ? 0 : (n - 1) * ns) + d);
+    return m_in || n_in;
+}
+
 li_status validate_rope(const li_rope_args *a) {
     if (!a) return fail(LI_ERR_INVALID_ARG, "args is NULL");
     const int e = dtype_bytes(a->dtype);
@@ -55,15 +62,9 @@ li_status validate_rope(const li_rope_args *a) {
         return fail(LI_ERR_INVALID_ARG, "x, y and positions must be aligned to their elements");
     if (a->x == a->y && (a->x_row_stride != a->y_row_stride || a->x_head_stride != a->y_head_stride))
         return fail(LI_ERR_INVALID_ARG, "in place, x and y must have the same strides");
-    // the elements of y are distinct where heads and rows do not overlap, in either order
-    const int64_t hs = a->y_head_stride, rs = a->y_row_stride;
-    const bool heads_in = (a->heads == 1 || hs >= a->head_dim) &&
-                          (a->rows == 1 || rs >= (a->heads - 1) * hs + a->head_dim);
-    const bool rows_in = (a->rows == 1 || rs >= a->head_dim) &&
-                         (a->heads == 1 || hs >= (a->rows - 1) * rs + a->head_dim);
-    if (!heads_in && !rows_in)
+    if (!apart(a->rows, a->y_row_stride, a->heads, a->y_head_stride, a->head_dim))
         return fail(LI_ERR_INVALID_ARG, "y's strides (%lld, %lld) make its elements overlap",
-                    (long long)rs, (long long)hs);
+                    (long long)a->y_row_stride, (long long)a->y_head_stride);
     return LI_OK;
 }
 
@@ -137,13 +138,9 @@ bool cache_has_rows(const li_cache_args *a) { return a->batch > 0 && a->x_len > 
 
 // Rows that li_cache_read writes must not overlap.
 li_status validate_cache_out(const li_cache_args *a) {
-    const bool tnd = a->layout_x == LI_LAYOUT_TND;
-    auto bad = [&](int64_t rs, int64_t bs, int d) {
-        if (a->x_len > 1 && rs < d) return true;
-        return !tnd && a->batch > 1 && bs < (a->x_len - 1) * (a->x_len > 1 ? rs : 0) + d;
-    };
-    if (bad(a->x_row_stride, a->x_batch_stride, a->dim) ||
-        (a->rope_dim > 0 && bad(a->rope_row_stride, a->rope_batch_stride, a->rope_dim)))
+    const int64_t n = a->layout_x == LI_LAYOUT_TND ? 1 : a->batch;
+    if (!apart(n, a->x_batch_stride, a->x_len, a->x_row_stride, a->dim) ||
+        (a->rope_dim > 0 && !apart(n, a->rope_batch_stride, a->x_len, a->rope_row_stride, a->rope_dim)))
         return fail(LI_ERR_INVALID_ARG, "the strides of x or rope make rows overlap");
     return LI_OK;
 }

@@ -27,3 +27,18 @@ def test_attention_without_rows_and_with_a_rope_part(B, S1, paged):
                              zeros(B, S1, 1, 4, dtype=torch.int32), 0.1, q_rope=zeros(B, S1, 16, 64, dtype=bf),
                              rope_cache=zeros(n, 9, 1, 64, dtype=bf), return_stats=True, **kw)
     assert [t.shape for t in out] == [(B, S1, 16, 128), (B, 1, S1, 16), (B, 1, S1, 16)]
+
+
+def test_read_into_rows_outside_batches():
+    """x as a (B, S, D) view of (S, B, D) storage, read and written."""
+    g = torch.Generator().manual_seed(1)
+    codes = torch.randn(3, 20, 1, 64, generator=g).to(torch.float8_e4m3fn).cuda()
+    scale = torch.rand(3, 20, generator=g).cuda() + 0.5
+    store = zeros(20, 3, 64)
+    out, _ = li.cache_read(codes, scale, store.transpose(0, 1))
+    assert torch.equal(out, codes.squeeze(2).float() * scale.unsqueeze(-1))
+    again, s2 = torch.zeros_like(codes), torch.zeros_like(scale)
+    li.cache_write(store.transpose(0, 1), again, s2)
+    want, ws = torch.zeros_like(codes), torch.zeros_like(scale)
+    li.cache_write(out.contiguous(), want, ws)
+    assert torch.equal(again.view(torch.uint8), want.view(torch.uint8)) and torch.equal(s2, ws)

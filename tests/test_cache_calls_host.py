@@ -1,5 +1,5 @@
-"""Calls of the cache entry points that have to be taken, without a GPU: pointers are fake, and nothing is
-launched or the launch fails for want of a device (LI_ERR_CUDA), which is not a refusal."""
+"""Calls of the cache entry points that have to be taken or refused, without a GPU: pointers are fake, and
+nothing is launched."""
 import ctypes
 
 import pytest
@@ -21,3 +21,9 @@ def test_attention_without_rows_needs_no_pointers(L, kw):
     """An empty tensor has no address: with a rope part as without."""
     for rope in (dict(), dict(Dr=64, q_rope=None, k_rope=0x70000), dict(Dr=64, q_rope=None, k_rope=None)):
         assert L.li_cache_attention(ctypes.byref(_cattn(**kw, **rope)), None, None, None, None) == 0, (kw, rope)
+
+
+@pytest.mark.parametrize("kw", [dict(x_batch_stride=127, x_row_stride=256), dict(x_batch_stride=128, x_row_stride=255),
+                                dict(x_batch_stride=1151, x_row_stride=128), dict(x_batch_stride=0, x_row_stride=128)])
+def test_read_refuses_batches_that_overlap(L, kw):
+    assert L.li_cache_read(ctypes.byref(_cache(**kw)), None) == 1, kw
