@@ -53,6 +53,11 @@ LAST_WAIT_TEST_FLAGS = ("-DLI_WAIT_LIMIT_NS=1000000ull", "-DLI_TEST_NO_LAST_COMM
 DEBUG_LIB = PKG / "libli_debug.so"
 DEBUG_FLAGS = ("-DLI_DEBUG=1",)
 
+# The same, with every buffer taken for one element shorter than it is: calls that touch the last element
+# of one must be seen to fail its check (and leave the access out).
+TIGHT_TEST_LIB = PKG / "libli_tighttest.so"
+TIGHT_TEST_FLAGS = ("-DLI_DEBUG=1", "-DLI_TEST_TIGHT_BOUNDS=1")
+
 
 def up_to_date(lib: Path = LIB) -> bool:
     if not lib.exists():
@@ -74,6 +79,11 @@ def build_last_wait_test(force: bool = False, verbose: bool = False) -> Path:
 def build_debug(force: bool = False, verbose: bool = False) -> Path:
     """libli_debug.so (see DEBUG_FLAGS)."""
     return build(force, verbose, DEBUG_FLAGS, lib=DEBUG_LIB, obj_sub="debug")
+
+
+def build_tight_test(force: bool = False, verbose: bool = False) -> Path:
+    """libli_tighttest.so (see TIGHT_TEST_FLAGS)."""
+    return build(force, verbose, TIGHT_TEST_FLAGS, lib=TIGHT_TEST_LIB, obj_sub="tighttest")
 
 
 def build(force: bool = False, verbose: bool = False, extra=(), lib: Path = LIB,
@@ -114,4 +124,5 @@ if __name__ == "__main__":
     build_wait_test(force="--force" in sys.argv, verbose="-v" in sys.argv)
     build_last_wait_test(force="--force" in sys.argv, verbose="-v" in sys.argv)
     build_debug(force="--force" in sys.argv, verbose="-v" in sys.argv)
+    build_tight_test(force="--force" in sys.argv, verbose="-v" in sys.argv)
     print(LIB)

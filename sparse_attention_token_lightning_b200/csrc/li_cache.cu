@@ -33,6 +33,7 @@ struct CacheParams {
     uint32_t *status;
     int64_t x_batch, x_row, r_batch, r_row;     // strides in elements
     int64_t bt_stride;
+    int64_t x_size, r_size, cache_rows;         // elements that x and rope span, rows of the cache
     int32_t rows, batch, x_len, k_len, num_blocks, block_size;
     int32_t dim, rope_dim;
     int32_t paged, lanes, lanes_log2;           // lanes per row
@@ -81,6 +82,12 @@ __device__ __forceinline__ void sequences_of(const CacheParams &P, int64_t r, in
     *hi = min(*lo + step, P.batch);
 }
 
+// Whether row r of the call lies inside x and rope.
+__device__ __forceinline__ bool row_ok(const CacheParams &P, int32_t r) {
+    return run_ok(row_offset(P, r, P.x_batch, P.x_row), P.dim, P.x_size, P.status) &&
+           (P.rope_dim == 0 || run_ok(row_offset(P, r, P.r_batch, P.r_row), P.rope_dim, P.r_size, P.status));
+}
+
 // Cache row of row r of the call (packed: of one of the sequences [lo, hi)), -1 where it takes no part:
 // past the rows in use, or data that does not fit, which is added to *err.
 __device__ __forceinline__ int64_t cache_row(const CacheParams &P, int32_t r, int32_t lo, int32_t hi, uint32_t *err) {
@@ -105,6 +112,7 @@ __device__ __forceinline__ int64_t cache_row(const CacheParams &P, int32_t r, in
         i = r - b * P.x_len;
         L1 = P.x_len;
     }
+    if (!idx_ok(b, (int64_t)P.batch + kBoundsSlack, P.status)) return -1;
     const int64_t cap = P.paged ? P.bt_stride * P.block_size : P.k_len;
     int64_t L2 = P.seqused_k ? __ldg(P.seqused_k + b) : P.k_len;
     if (L2 < 0 || L2 > cap) *err |= LI_DEVERR_LENGTHS;
@@ -121,6 +129,7 @@ __device__ __forceinline__ int64_t cache_row(const CacheParams &P, int32_t r, in
     }
     if (!P.paged) return (int64_t)b * P.k_len + pos;
     const int32_t q = P.by_block.div((int32_t)pos);         // pos is below the int32 L2
+    if (!idx_ok((int64_t)b * P.bt_stride + q, (int64_t)P.batch * P.bt_stride, P.status)) return -1;
     const int32_t blk = __ldg(P.block_table + (int64_t)b * P.bt_stride + q);
     if (blk < 0 || blk >= P.num_blocks) {
         *err |= LI_DEVERR_TABLE;
@@ -231,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
     int64_t slot = -1;
     typename MaxOf<T>::type m2{};
     const T *rope = static_cast<const T *>(P.rope);
-    if (r < P.rows) {
+    if (r < P.rows && row_ok(P, (int32_t)r)) {
         const T *x = static_cast<const T *>(P.x) + row_offset(P, (int32_t)r, P.x_batch, P.x_row) + 8 * lane;
 #pragma unroll
         for (int k = 0; k < kSteps; ++k)
@@ -242,6 +251,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
         }
         uint32_t err = 0;
         slot = cache_row(P, (int32_t)r, 0, P.batch, &err);
+        if (slot >= 0 && !idx_ok(slot, P.cache_rows, P.status)) slot = -1;
         report(P, err);
 #pragma unroll
         for (int k = 0; k < kSteps; ++k)
@@ -299,7 +309,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
     uint32_t err = 0;
     const int64_t slot = cache_row(P, (int32_t)r, lo, hi, &err);
     report(P, err);
-    if (slot < 0) return;
+    if (slot < 0 || !idx_ok(slot, P.cache_rows, P.status) || !row_ok(P, (int32_t)r)) return;
     const float s = __ldg(P.descale + slot);
     const uint8_t *codes = P.codes + slot * P.dim + 8 * lane;
     const T *rc = reinterpret_cast<const T *>(P.rope_cache) + slot * P.rope_dim + 8 * lane;
@@ -356,6 +366,10 @@ CacheParams params(const li_cache_args &a) {
     P.r_batch = a.rope_batch_stride;
     P.r_row = a.rope_row_stride;
     P.bt_stride = a.block_table_stride;
+    const int64_t outer = P.cu_seqlens ? 0 : a.batch - 1;
+    P.x_size = outer * a.x_batch_stride + (a.x_len - 1) * a.x_row_stride + a.dim;
+    P.r_size = outer * a.rope_batch_stride + (a.x_len - 1) * a.rope_row_stride + a.rope_dim;
+    P.cache_rows = a.layout_k == LI_LAYOUT_PA_BSND ? (int64_t)a.num_blocks * a.block_size : (int64_t)a.batch * a.k_len;
     P.rows = P.cu_seqlens ? a.x_len : a.batch * a.x_len;
     P.batch = a.batch;
     P.x_len = a.x_len;

@@ -319,6 +319,16 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
 }
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
+// Entry `at` of all rows' selections; the bounds-checked build takes one outside for none.
+__device__ __forceinline__ int32_t entry(const Params &P, int64_t at) {
+    return idx_ok(at, (int64_t)P.rows * P.topk, P.status) ? __ldg(P.indices + at) : -1;
+}
+// Block q of batch b's sequence.
+__device__ __forceinline__ int32_t block_of(const Params &P, int32_t b, int32_t q) {
+    const int64_t at = b * P.bt_stride + q;
+    return idx_ok(at, (int64_t)P.by_s1.div(P.rows) * P.bt_stride, P.status) ? __ldg(P.block_table + at) : -1;
+}
+
 // One warp: the tiles of each unit (those behind its last selected entry are left out), and for each
 // tile the cache rows of its keys, four a lane, with their scales on the way into shared memory.
 __device__ void lookup_role(const Params &P, Tail *T, const Bars &bars) {
@@ -329,26 +339,26 @@ __device__ void lookup_role(const Params &P, Tail *T, const Bars &bars) {
     for (int it = 0; ok; ++it) {
         const Unit u = unit_at(P, it);
         if (u.row < 0) break;
-        const int32_t *ir = P.indices + (int64_t)u.row * P.topk;
+        const int64_t first = (int64_t)u.row * P.topk;
         const int32_t b = P.by_s1.div(u.row);
         const int32_t *table = P.block_table ? P.block_table + b * P.bt_stride : nullptr;
         const int from = u.tile0 * kKeys, to = min((u.tile0 + u.tiles) * kKeys, P.topk);
-        const int32_t tail = __ldg(ir + to - 1);
+        const int32_t tail = entry(P, first + to - 1);
         int32_t v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int p = from + lane + 32 * i;
-            v[i] = p < to ? __ldg(ir + p) : -1;
+            v[i] = p < to ? entry(P, first + p) : -1;
         }
         // the rest of the unit's entries, and the start of its block-table row, on their way to L2
-        for (int p = from + kKeys + 32 * lane; p < to; p += 32 * 32) prefetch_l2(ir + p);
+        for (int p = from + kKeys + 32 * lane; p < to; p += 32 * 32) prefetch_l2(P.indices + first + p);
         if (table && 32 * lane < P.bt_stride) prefetch_l2(table + 32 * lane);
         int tiles = u.tiles;
         if (tail < 0) {
             int last = -1;
 #pragma unroll 8
             for (int p = from + lane; p < to; p += 32)
-                if (__ldg(ir + p) >= 0) last = p;
+                if (entry(P, first + p) >= 0) last = p;
             last = __reduce_max_sync(0xffffffffu, last);
             tiles = last < from ? 0 : (last - from) / kKeys + 1;
         }
@@ -369,12 +379,12 @@ __device__ void lookup_role(const Params &P, Tail *T, const Bars &bars) {
                 if (!in && v[i] >= 0) err |= LI_DEVERR_LENGTHS;
                 const int32_t q = table && in ? P.by_block.div(v[i]) : 0;
                 off[i] = in ? v[i] - q * P.block_size : -1;
-                blk[i] = table && in ? __ldg(table + q) : b;
+                blk[i] = table && in ? block_of(P, b, q) : b;
             }
             // the next tile's entries
             const int next = from + (j + 1) * kKeys + lane;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = next + 32 * i < to ? __ldg(ir + next + 32 * i) : -1;
+            for (int i = 0; i < 4; ++i) v[i] = next + 32 * i < to ? entry(P, first + next + 32 * i) : -1;
             ok = wait_warp(bars.looked_up(tr.idx), tr.phase ^ 1u, &T->abort_flag);
             if (!ok) break;
 #pragma unroll
@@ -714,6 +724,7 @@ __device__ __forceinline__ void lds4(const float *p, float (&v)[4]) {
 // NaN out and the sum does not: a NaN there is the maximum's too.
 __device__ __forceinline__ void store_stats(const Params &P, int64_t at, float m, float sum, float ref) {
     const float kInf = __int_as_float(0x7f800000);
+    if (!idx_ok(at, (int64_t)P.rows * P.G, P.status)) return;
     P.smax[at] = sum != sum ? sum : m > -kInf ? m * kLn2 : m;
     P.ssum[at] = m > -kInf ? sum * exp2_(ref - m) : sum;
 }

@@ -358,9 +358,19 @@ __device__ __forceinline__ bool in_bounds(bool ok, uint32_t *status) {
     }
     return true;
 }
-// Index i of a buffer of n elements.
+// Index i of a buffer of n elements. (One test build takes every buffer for an element shorter than it
+// is, so that checks can be seen to fail on calls that touch nothing but their own.)
+#ifdef LI_TEST_TIGHT_BOUNDS
+constexpr int kBoundsSlack = 1;
+#else
+constexpr int kBoundsSlack = 0;
+#endif
 __device__ __forceinline__ bool idx_ok(int64_t i, int64_t n, uint32_t *status) {
-    return in_bounds(i >= 0 && i < n, status);
+    return in_bounds(i >= 0 && i < n - kBoundsSlack, status);
+}
+// Elements [i, i + run) of such a buffer.
+__device__ __forceinline__ bool run_ok(int64_t i, int64_t run, int64_t n, uint32_t *status) {
+    return in_bounds(i >= 0 && i + run <= n - kBoundsSlack, status);
 }
 
 // Sets the message li_last_error_string() returns on this host thread.

@@ -33,6 +33,7 @@ struct RopeParams {
     void *y;
     const void *positions;
     int64_t x_row, x_head, y_row, y_head;
+    int64_t x_size, y_size;             // elements that they span
     int32_t rows, heads, head_dim, pairs, offset;
     int32_t rows_per_block;
     int32_t rotated, copies;            // items of a head
@@ -53,6 +54,12 @@ template <> __device__ __forceinline__ float from_f32(float v) { return v; }
 
 // kVec elements of T in one access.
 template <class T, int kVec> struct alignas(sizeof(T) * kVec) Vec { T v[kVec]; };
+
+// Whether an access of kVec elements at `from` of x and `to` of y lies inside them. There is no status word
+// here: the bounds-checked build leaves the access out.
+template <int kVec> __device__ __forceinline__ bool access_ok(const RopeParams &P, int64_t from, int64_t to) {
+    return run_ok(from, kVec, P.x_size, nullptr) && run_ok(to, kVec, P.y_size, nullptr);
+}
 
 // Item t of the block's rows: element offsets of its access in x and y, its row and item in the head.
 struct Place {
@@ -110,11 +117,15 @@ __global__ void __launch_bounds__(kThreads, kPairs ? 8 : 6) rope_kernel(const __
             int d = p.e * kVec;
             if (d >= P.offset) d += 2 * P.pairs;
             to[k] = p.to + d;
+            if (!access_ok<kVec>(P, p.from + d, to[k])) {
+                to[k] = -1;
+                continue;
+            }
             a[k] = *reinterpret_cast<const V *>(x + p.from + d);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (t0 + k * kThreads < copies) *reinterpret_cast<V *>(y + to[k]) = a[k];
+            if (t0 + k * kThreads < copies && (!kDebugBounds || to[k] >= 0)) *reinterpret_cast<V *>(y + to[k]) = a[k];
     }
     __syncthreads();
     const uint32_t items = (uint32_t)nrow * P.heads * P.rotated;
@@ -130,12 +141,18 @@ __global__ void __launch_bounds__(kThreads, kPairs ? 8 : 6) rope_kernel(const __
             const int d = P.offset + p.e * P.u_step;
             angle[k] = p.r * P.pairs + p.e * (kPairs ? kVec : kVec / 2);
             to[k] = p.to + d;
+            if (!access_ok<kVec>(P, p.from + d, to[k]) ||
+                (kPairs && !access_ok<kVec>(P, p.from + d + P.v_step, to[k] + P.v_step)) ||
+                !run_ok(angle[k], kPairs ? kVec : kVec / 2, (int64_t)P.rows_per_block * P.pairs + kBoundsSlack, nullptr)) {
+                to[k] = -1;
+                continue;
+            }
             a[k] = *reinterpret_cast<const V *>(x + p.from + d);
             if (kPairs) b[k] = *reinterpret_cast<const V *>(x + p.from + d + P.v_step);
         }
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-            if (t0 + k * kThreads >= items) continue;
+            if (t0 + k * kThreads >= items || (kDebugBounds && to[k] < 0)) continue;
             const float2 *ang = cs + angle[k];
             if constexpr (kPairs) {
 #pragma unroll
@@ -208,6 +225,8 @@ cudaError_t launch_rope(const li_rope_args &a, bool grad, cudaStream_t st) {
     P.x_head = a.x_head_stride;
     P.y_row = a.y_row_stride;
     P.y_head = a.y_head_stride;
+    P.x_size = (a.rows - 1) * P.x_row + (a.heads - 1) * P.x_head + a.head_dim;
+    P.y_size = (a.rows - 1) * P.y_row + (a.heads - 1) * P.y_head + a.head_dim;
     P.rows = (int32_t)a.rows;
     P.heads = a.heads;
     P.head_dim = a.head_dim;
