@@ -8,6 +8,10 @@ indexer over host-resident problems with the copies overlapping the kernels. ``r
 ``rope_grad()`` rotate queries and keys, ``cache_write()`` / ``cache_read()`` keep keys as E4M3
 codes with a scale per row and ``cache_attention()`` attends over selected rows of such a cache.
 There is no fallback: if the library is missing, loading raises.
+
+No call here is recorded by autograd: outputs have no history, also where an input requires grad.
+Gradients are calls of their own (``kl_grad()``, ``rope_grad()``), for the backward of a
+``torch.autograd.Function`` of the caller's.
 """
 from __future__ import annotations
 
@@ -632,7 +636,10 @@ def rope(x, positions, freqs: RopeFrequencies, offset: int = 0, interleaved: boo
          out=None, stream=None):
     """Rotary positions (li_rope) of x (..., heads, head_dim), bf16, fp16 or fp32, at positions
     (...), int32 or int64: elements [offset, offset + freqs.rope_dim) of every head are rotated,
-    the others copied. `out` may be x (in place). Leading dimensions and heads may be strided."""
+    the others copied. `out` may be x (in place); otherwise it must not overlap x. Leading dimensions
+    and heads may be strided, so the rotated part can go straight to the contiguous tensor that
+    cache_attention() takes as q_rope: rope(q[..., 512:], positions, freqs, out=q_rope). The output
+    has no autograd history (see rope_grad)."""
     return _rope(lib().li_rope, x, positions, freqs, offset, interleaved, out, stream)
 
 
@@ -753,7 +760,7 @@ def cache_write(x, codes, descale, rope=None, rope_cache=None, seqused_k=None, b
 
     x (B, S, D), or (T, D) with cu_seqlens (B + 1,), bf16 / fp16 / fp32, rows may be strided (a
     head dimension of 1 before D is taken too); codes float8_e4m3fn and descale fp32, paged
-    (num_blocks, block_size, 1, D) / (num_blocks, block_size) with block_table (B, width) and
+    (num_blocks, block_size, 1, D) / (num_blocks, block_size) with block_table (B, width), contiguous, and
     seqused_k (B,), or dense (B, S2, 1, D) / (B, S2). Row i of batch b is key position
     seqused_k[b] - rows_b + i, rows_b = seqused[b] (all rows when None). rope / rope_cache: a part
     of each row kept in its own type. pow2: power-of-two scales. The cache is li_indexer's
@@ -818,7 +825,7 @@ def cache_attention(q, codes, descale, sparse_indices, scale, q_rope=None, rope_
                     stream=None, check: bool = True):
     """Attention of q (B, S1, G, Dm), bf16, over selected rows of an E4M3 cache
     (li_cache_attention): codes / descale / rope_cache as cache_write fills them, paged with
-    block_table (s2: the positions it may address, its whole width when None) or dense;
+    block_table, contiguous (s2: the positions it may address, its whole width when None), or dense;
     sparse_indices (B, S1, 1, topk) as li_indexer returns them without offsets. Returns out (B, S1,
     G, Dm) bf16, or (out, softmax_max, softmax_sum) with return_stats, (B, 1, S1, G) fp32."""
     a = make_cache_attn_args(q, codes, descale, sparse_indices, scale, q_rope, rope_cache,

@@ -42,3 +42,33 @@ def test_read_into_rows_outside_batches():
     want, ws = torch.zeros_like(codes), torch.zeros_like(scale)
     li.cache_write(out.contiguous(), want, ws)
     assert torch.equal(again.view(torch.uint8), want.view(torch.uint8)) and torch.equal(s2, ws)
+
+
+def test_the_rotated_part_goes_straight_to_q_rope():
+    """The rotated part of a fused query into a tensor of its own, as cache_attention() takes it."""
+    g = torch.Generator().manual_seed(2)
+    q = torch.randn(2, 3, 16, 192, generator=g).to(torch.bfloat16).cuda()
+    pos, freqs = torch.arange(6, device="cuda").view(2, 3), li.rope_frequencies(64)
+    whole = li.rope(q, pos, freqs, offset=128, interleaved=True)
+    part = li.rope(q[..., 128:], pos, freqs, interleaved=True, out=torch.empty_like(q[..., 128:]).contiguous())
+    assert part.is_contiguous() and torch.equal(part, whole[..., 128:])
+
+
+def test_no_call_is_recorded_by_autograd():
+    """Outputs have no history, also of inputs that require grad; rope_grad() is the rotation's gradient."""
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(5, 2, 64, generator=g).cuda().requires_grad_()
+    pos, freqs = torch.arange(5, device="cuda"), li.rope_frequencies(64)
+
+    class Rope(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return li.rope(x, pos, freqs)
+
+        @staticmethod
+        def backward(ctx, dy):
+            return li.rope_grad(dy.contiguous(), pos, freqs)
+    assert not li.rope(x, pos, freqs).requires_grad
+    dy = torch.randn(5, 2, 64, generator=g).cuda()
+    Rope.apply(x).backward(dy)
+    assert torch.equal(x.grad, li.rope_grad(dy, pos, freqs)) and x.grad.abs().sum() > 0
