@@ -4,15 +4,12 @@
 // second call runs on a stream) and their metadata-then-indexer order (lightning_indexer,
 // "Prototype").
 #include <atomic>
-#include <cstdarg>
-#include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <string>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "li_attn.cuh"
+#include "li_host.cuh"
 #include "li_internal.cuh"
 #include "li_kl.cuh"
 #include "li_merge.cuh"
@@ -20,22 +17,9 @@
 
 namespace {
 
+using namespace li::host;
+
 thread_local std::string g_err;
-
-li_status fail(li_status st, const char *fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_err = buf;
-    return st;
-}
-
-li_status ok() {
-    g_err.clear();
-    return LI_OK;
-}
 
 cudaEvent_t g_stage_events[6] = {};
 bool g_stage_events_on = false;
@@ -43,18 +27,6 @@ bool g_stage_events_on = false;
 void stage_mark(int i, cudaStream_t st) {
     if (g_stage_events_on && g_stage_events[i]) cudaEventRecord(g_stage_events[i], st);
 }
-
-// NVTX range around each entry point and each stage it enqueues, for timeline tools (Nsight
-// Systems); without a tool attached a push/pop pair costs a few nanoseconds. Building with
-// -DNVTX_DISABLE compiles them out.
-struct NvtxRange {
-    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange &) = delete;
-    NvtxRange &operator=(const NvtxRange &) = delete;
-};
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Which score kernel runs: the tensor-core kernel unless LI_SCORE_KERNEL=simple selects the
 // CUDA-core one (a debugging switch; both write the same score rows).

@@ -11,12 +11,11 @@
 // 128 are written in 6.8 us (1.9): one wave of blocks, whose time is a row's chain of reads (its
 // sequence, lengths, block) and some 10 instructions an element; 1120 rows are read in 3.0, most of
 // it the launch.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "li_cache.cuh"
 #include "li_fixed_div.cuh"
+#include "li_float.cuh"
 
 namespace li {
 namespace {
@@ -137,14 +136,6 @@ __device__ __forceinline__ int64_t cache_row(const CacheParams &P, int32_t r, in
     }
     return (int64_t)blk * P.block_size + ((int32_t)pos - q * P.block_size);
 }
-
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-template <class T> __device__ __forceinline__ T from_f32(float v);
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
-template <> __device__ __forceinline__ float from_f32(float v) { return v; }
 
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) < __int_as_float(0x7f800000); }
 

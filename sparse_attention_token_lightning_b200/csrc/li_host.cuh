@@ -28,6 +28,8 @@ inline li_status ok() {
 }
 inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// NVTX range around each entry point and each stage it enqueues, for timeline tools; without a tool
+// attached a push/pop pair costs a few nanoseconds. Building with -DNVTX_DISABLE compiles them out.
 struct NvtxRange {
     explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
     ~NvtxRange() { nvtxRangePop(); }

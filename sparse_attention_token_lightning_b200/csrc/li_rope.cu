@@ -9,9 +9,7 @@
 // less its nearest integer) and only the remainder, at most half a turn, goes through fp32, so a
 // position of 2^20 is as accurate as position 1; a table per row instead of a table of all
 // positions costs no memory traffic and no limit on positions.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
+#include "li_float.cuh"
 #include "li_rope.cuh"
 
 namespace li {
@@ -43,14 +41,6 @@ struct RopeParams {
     float magnitude, sign;              // sign of sin: -1 for the gradient
     double turns[LI_ROPE_MAX_PAIRS];    // freq / 2 pi
 };
-
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-template <class T> __device__ __forceinline__ T from_f32(float v);
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
-template <> __device__ __forceinline__ float from_f32(float v) { return v; }
 
 // kVec elements of T in one access.
 template <class T, int kVec> struct alignas(sizeof(T) * kVec) Vec { T v[kVec]; };
