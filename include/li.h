@@ -571,7 +571,8 @@ li_status li_cache_read(const li_cache_args *args, void *stream);
  * Numerics: q and the softmax weights enter the products as two E4M3 parts each, the codes as they
  * are, sums in fp32. q is exact down to 2^-13 of its head's largest element and off by at most 2^-21
  * of that below, so the scores have fp32 accuracy; a weight exp(x - m) descale_s is off by at most
- * 1.25 x 2^-9 of itself or 2^-21 of the row's largest, whichever is more; the normaliser sums the
+ * 1.25 x 2^-9 of itself or 2^-21 of the row's largest, whichever is more (a key of zeros counts
+ * there with its scale, 1 as li_cache_write leaves it); the normaliser sums the
  * unrounded weights exp(x - m), whatever scales within the limits a row's keys have.
  * No workspace. Stream-ordered, no allocation, graph-capturable, deterministic (bit-identical reruns
  * on one device model).

@@ -6,10 +6,10 @@
 //
 // A row belongs to a group of lanes, eight elements a lane and step, and stays in registers between
 // its maximum (a shuffle reduction) and its codes, so it is read from memory once. Bound by memory:
-// 57344 rows of 512 + 64 bf16 values are written in 21.1 us
+// 57344 rows of 512 + 64 bf16 values are written in 21.2 us
 // (103 MB, 4.9 TB/s; at a copy's 6.5 TB/s 15.7), 53248 read back in 18.4 (96 MB, 5.2 TB/s). 32768 keys of
-// 128 are written in 6.8 us (1.9): one wave of blocks, whose time is a row's chain of reads (its
-// sequence, lengths, block) and some 10 instructions an element; 1120 rows are read in 3.0, most of
+// 128 are written in 7.2 us (1.9): one wave of blocks, whose time is a row's chain of reads (its
+// sequence, lengths, block) and some 10 instructions an element; 1120 rows are read in 3.2, most of
 // it the launch.
 #include <cuda_fp8.h>
 
@@ -66,8 +66,8 @@ __device__ __forceinline__ int64_t row_offset(const CacheParams &P, int32_t r, i
 // The packed sequences among which row r lies, [*lo, *hi): one of 32 ranges, found by the warp at once
 // (its rows are neighbours, and 32 reads side by side take as long as one step of a search). All lanes
 // call; rows outside the call get any. For the read, which waits for its place (1120 rows of 32
-// sequences 3.3 us against 3.6, at 256 threads a block); the write has its rows to read meanwhile, and the votes cost it more
-// (32768 rows 8.8 against 7.8).
+// sequences 3.2 us against 3.5); the write has its rows to read meanwhile, and the votes cost it more
+// (32768 rows 7.6 against 7.0).
 __device__ __forceinline__ void sequences_of(const CacheParams &P, int64_t r, int32_t *lo, int32_t *hi) {
     const int lane = threadIdx.x & 31, step = (P.batch + 31) / 32, at = (lane + 1) * step;
     const int32_t start = at < P.batch ? __ldg(P.cu_seqlens + at) : INT32_MAX;
@@ -334,10 +334,10 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
 }
 
 // Elements of a lane, at most (dim allowing). A row's address work is shared by them, and the kernels
-// are bound by instructions when there are many rows: 32 rather than 16 write 57344 rows of 512 in 21.1 us
-// against 26.9, read 53248 in 18.4 against 21.4 and write 32768 of 128 in 6.8 against 7.5. Where the
+// are bound by instructions when there are many rows: 32 rather than 16 write 57344 rows of 512 in 21.2 us
+// against 27.4, read 53248 in 18.4 against 21.6 and write 32768 of 128 in 7.2 against 7.8. Where the
 // elements do not fill the SMs' threads at 8 a thread, more threads hide more latency: 1120 rows of 128
-// read in 3.0 us against 4.0, 64 of 512 written in 2.5 against 2.9. (Blocks of 256 threads: 0.2 us more.)
+// read in 3.2 us against 3.6, 64 of 512 written in 2.5 against 2.6. (Blocks of 256 threads: 0.1 to 0.2 us more.)
 int per_lane(int64_t rows, int dim) { return rows * dim > (int64_t)device_sm_count() * 2048 * 8 ? 32 : 16; }
 
 CacheParams params(const li_cache_args &a) {

@@ -31,18 +31,21 @@
 //   gather    copies codes and rope part with cp.async into 16 KB slots (128 keys x 128 bytes,
 //             128-byte swizzle); rows that select nothing are zero-filled
 //   qk, pv    one thread each issues the two products
-// Measured (576 values a key, 16 heads; graph replay on one B200): 64 sequences x 2048 keys 25.6 us (85 MB
-// of selected rows, 3.3 TB/s; what memory alone takes is 13.3), one sequence 12.5, causal 2048 tokens x 1024
-// keys 168 us (1.05 GB out of L2, 6.3 TB/s), 21 rows x 777 keys x 128 heads of 256 19.5 us.
-// A tile then costs a CTA some 3700 cycles, of which no unit is full: the gather alone takes 2140 (38
+// Measured (576 values a key, 16 heads; graph replay on one B200): 64 sequences x 2048 keys 25.9 to 28.0 us
+// by box (85 MB of selected rows, 3.3 TB/s at best; what memory alone takes is 13.3), one sequence 13.0, causal
+// 2048 tokens x 1024 keys 179 us (1.05 GB out of L2, 5.9 TB/s), 21 rows x 777 keys x 128 heads of 256 21
+// us, 64 rows x 2048 keys x 128 heads 83.
+// A tile then costs a CTA some 3900 cycles, of which no unit is full: the gather alone takes 2140 (38
 // bytes a cycle and SM, for 16 SMs as for 148), the operands of the products 150 KB of shared memory
-// (1500 cycles), a softmax from scores to weights 2000. More overlap did not help: with tiles of 64 keys
-// the 2048 tokens took 247 us where these took 205, with twice the softmax warps on alternate tiles 209
-// against 184, with eight gather warps 183, with TMA's gather for two of five slots more than either.
-// Shorter code did: the roles' code shares the instruction caches, and its loops are kept (226 us at 110
-// KB of code, 205 at 87, 184 at 79, 172 at 71), as did room for more slots (201 against 186).
+// (1500 cycles), a softmax from scores to weights 2000. More overlap did not help (figures of the builds in
+// which it was tried, each against the build before it): with tiles of 64 keys the 2048 tokens took 247 us
+// where these took 205, with twice the softmax warps on alternate tiles 209 against 184, with eight gather
+// warps 183, with TMA's gather for two of five slots more than either. Shorter code did: the roles' code
+// shares the instruction caches, and its loops are kept (226 us at 110 KB of code, 205 at 87, 184 at 79, 172 at
+// 71), as did room for more slots (201 against 186).
 // Every wait is bounded in time; on expiry the kernel records LI_DEVERR_TIMEOUT and returns. The
-// softmax warps of a group agree on giving up (the vote carries it), so none is left at a barrier.
+// softmax warps of a group agree on giving up (the vote carries it), so none is left at a barrier; a wait for a
+// unit's last product, which no vote follows, is told by the warp that made it.
 #include <atomic>
 
 #include <cuda_bf16.h>
@@ -878,7 +881,7 @@ __device__ void softmax_role(const Params &P, uint8_t *smem, Tail *T, const Bars
                     ok = ok && wait_lane(bars.p_empty(b ^ 1u), ((kt - 1) >> 1) & 1u, abort_flag);
                     __syncwarp();
                     tc_fence_after();
-                    // two reads in flight where the registers allow (2048 tokens 168 us against 171)
+                    // two reads in flight where the registers allow (2048 tokens 179 us against 183)
                     constexpr int kB = 16 / H;
 #pragma unroll 1
                     for (int c = 0; c < 2 * P.blocks; c += kB) {    // hi and lo of each block
@@ -1205,11 +1208,12 @@ bool cache_attn_plan(const li_cache_attn_args &a, CacheAttnPlan *p) {
     // CTAs per unit: as many as leave every unit its SMs at once and every CTA a tile, if that spares
     // a CTA two tiles or more. A cluster lies in one GPC, whose SMs do not divide by it: 74 clusters of
     // two find room on 148 SMs, 33 of four and 15 of eight.
-    // Shared against whole, 16 heads: 1 row of 2048 entries 12.9 us and 29.2, 14 rows 13.7 and 29.2, 32
-    // rows (four CTAs each) 16.8 and 29.6, 74 rows (two) 23.9 and 32.2; 512 entries, 1 row 10.3 and
-    // 11.6, 74 rows 13.1 and 13.3. Where only one tile is spared sharing loses: 192 entries, 74 rows
-    // 11.4 and 9.8. Partial outputs through memory and a second kernel took 13.1, 15.7 (16 rows) and
-    // 24.8 us (74), with 5 us more on the host.
+    // Shared against whole, 16 heads of 576, sequences of 16384 keys: 1 row of 2048 entries 12.9 us and 29.0,
+    // 14 rows 14.3 and 30.8, 32 rows (four CTAs each) 19.3 and 32.2, 74 rows (two) 27.8 and 34.1; 512
+    // entries, 1 row 10.4 and 12.5, 32 rows 12.2 and 13.1, 74 rows 15.1 and 14.6. One row more than finds
+    // room costs a second wave: 16 rows with eight CTAs 26.3 (four: 16.4), 36 with four 33.7 (two: 23.4), 75
+    // with two 46.0 (whole: 34.3). Where only one tile is spared sharing loses: 192 entries, 74 rows 11.7 and
+    // 10.2. Partial outputs through memory and a second kernel cost 5 us more on the host.
     constexpr int kHalfSms[kMaxCutLog2 + 1] = {2, 4, 9, 20};    // half SMs that a cluster takes
     p->cut_log2 = kMaxCutLog2;
     while (p->cut_log2 > 0 && (p->units * kHalfSms[p->cut_log2] > 2 * (int64_t)sms || p->tiles >> p->cut_log2 == 0)) --p->cut_log2;
