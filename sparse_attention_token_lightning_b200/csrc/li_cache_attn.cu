@@ -32,7 +32,7 @@
 //             128-byte swizzle); rows that select nothing are zero-filled
 //   qk, pv    one thread each issues the two products
 // Measured (576 values a key, 16 heads; graph replay on one B200): 64 sequences x 2048 keys 25.9 to 28.0 us
-// by box (85 MB of selected rows, 3.3 TB/s at best; what memory alone takes is 13.3), one sequence 13.0, causal
+// by machine (85 MB of selected rows, 3.3 TB/s at best; what memory alone takes is 13.3), one sequence 13.0, causal
 // 2048 tokens x 1024 keys 179 us (1.05 GB out of L2, 5.9 TB/s), 21 rows x 777 keys x 128 heads of 256 21
 // us, 64 rows x 2048 keys x 128 heads 83.
 // A tile then costs a CTA some 3900 cycles, of which no unit is full: the gather alone takes 2140 (38
